@@ -39,6 +39,14 @@
  *   hipStream_t; NULL is the default stream).  Data-dependent decode errors
  *   are reported through a device status word (see pc_decode).
  *
+ * Stored tensors ("Q8") and the operators of a training step that use them
+ *   The bytes the coder takes come from somewhere and go somewhere: the
+ *   second half of this file stores a tensor of a training step as e4m3 or
+ *   int8 symbols with one power-of-two scale for every 32 columns (the
+ *   symbols are what pc_encode codes and pc_histogram counts), and uses the
+ *   symbols, as pc_decode gives them back, in the backward pass and as an
+ *   embedding table.
+ *
  * Memory
  *   The library never allocates.  Every buffer belongs to the caller; device
  *   pointers must stay valid until the stream has executed the call.
@@ -321,6 +329,146 @@ pc_status pc_histogram(const uint8_t *d_in, size_t n, uint64_t *d_counts, void *
  * `stream`; bytes == 0 does nothing.
  */
 pc_status pc_traffic_probe(const void *d_src, void *d_dst, size_t bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Tensors stored in 8 bits, and the operators that use them
+ *
+ * A stored tensor ("Q8") of rows x cols elements is
+ *   sym    one byte per element, rows of cols bytes; row r starts at
+ *          sym + r * ld_sym.  Dense (ld_sym == cols) it is the byte string
+ *          that pc_encode takes.
+ *   scale  one code per group of 32 columns (the last group of a row may be
+ *          short); row r starts at scale + r * ld_scale.
+ * The element in row r and column c stands for
+ *          element(sym[r][c]) * 2^(scale[r][c / 32] - 127),
+ * element() being OCP E4M3FN or int8 two's complement.  A byte that stands
+ * for no number (0x7F and 0xFF in e4m3, 0x80 in int8) reads as NaN.  Powers
+ * of two keep every stored value exact in bf16 and f32, so the matrix
+ * instructions multiply stored values without rounding them again.  Scale
+ * codes run from 1 to 254; pc_q8_store writes 10 to 248.
+ *
+ * Tensors of plain numbers are f32, f16 or bf16, rows of unit stride and a
+ * row distance `ld` in elements that may exceed the width; pointers need the
+ * alignment of their element only.  All arithmetic is in 32 bits, rounded
+ * once to the output's type.  Inputs and outputs must not overlap unless an
+ * entry says so.  Every entry is asynchronous on `stream`, allocates
+ * nothing, keeps nothing between calls, and gives the same bits every time.
+ * ------------------------------------------------------------------------ */
+
+#define PC_Q8_GROUP 32
+
+typedef enum pc_dtype { PC_F32 = 0, PC_F16 = 1, PC_BF16 = 2 } pc_dtype;
+
+typedef enum pc_q8_format {
+    PC_Q8_E4M3 = 0, /* largest magnitude 448 */
+    PC_Q8_INT8 = 1  /* -127 .. 127 */
+} pc_q8_format;
+
+typedef enum pc_activation {
+    PC_ACT_SILU = 0,     /* x / (1 + exp(-x)) */
+    PC_ACT_GELU = 1,     /* x Phi(x), Phi the normal distribution function */
+    PC_ACT_GELU_TANH = 2 /* x/2 (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
+} pc_activation;
+
+/* A stored tensor in device memory, as an argument (the struct itself is host memory, read during the call). */
+typedef struct pc_q8 {
+    const uint8_t *sym;
+    const uint8_t *scale;
+    uint64_t rows, cols;
+    uint64_t ld_sym;   /* >= cols */
+    uint64_t ld_scale; /* >= ceil(cols / 32) */
+    int32_t format;    /* pc_q8_format */
+    int32_t reserved;  /* 0 */
+} pc_q8;
+
+/*
+ * Store a tensor in 8 bits.  For each group of 32 columns of a row, with a
+ * the largest finite magnitude in it and M the format's (448 or 127):
+ *   k = the smallest integer >= -117 with a <= M 2^k  (-117 where a is 0)
+ *   sym = x 2^-k rounded to the nearest element, ties to even;  code = k + 127
+ * so no finite value saturates.  Infinities and NaN take no part in a and
+ * become 0x7F (e4m3) or 0x80 (int8), which read back as NaN.
+ *   d_x       rows x cols, row distance ldx.
+ *   d_sym     rows * cols bytes, dense.
+ *   d_scale   rows * ceil(cols / 32) bytes, dense.
+ *   d_counts  NULL, or 256 u64 (8-byte aligned) to which the histogram of
+ *             the symbols is added, as pc_histogram would, in the same pass:
+ *             the statistics a codebook is built from.
+ * rows == 0 or cols == 0 does nothing.  cols is below 2^31.
+ */
+pc_status pc_q8_store(const void *d_x, int dtype, size_t rows, size_t cols, size_t ldx, int format,
+                      uint8_t *d_sym, uint8_t *d_scale, uint64_t *d_counts, void *stream);
+
+/* Read a stored tensor back: d_out (rows x cols, row distance ld_out) = the values, rounded to dtype. */
+pc_status pc_q8_load(const pc_q8 *q, void *d_out, int dtype, size_t ld_out, void *stream);
+
+/*
+ * Backward pass of an activation whose inputs were stored.  With g and u the
+ * stored gate and up values and dh the gradient of h:
+ *   h = act(g) u,   d_gate = dh u act'(g),   d_up = dh act(g);
+ * with up == NULL (an activation without a gate)  h = act(g), d_gate = dh act'(g).
+ *   d_dh     rows x cols, as are the outputs; all of one dtype, each with a
+ *            row distance of its own.  d_gate may be d_dh itself (same ld).
+ *   gate, up stored tensors of that size and of one format; to read gate and
+ *            up out of one tensor that holds them side by side, point into it.
+ *   d_up     NULL exactly where up is NULL.
+ *   d_h      NULL, or receives h (for the weight gradient of what follows).
+ */
+pc_status pc_q8_glu_backward(const void *d_dh, int dtype, size_t ld_dh, const pc_q8 *gate, const pc_q8 *up,
+                             int activation, void *d_gate, size_t ld_gate, void *d_up, size_t ld_up, void *d_h,
+                             size_t ld_h, void *stream);
+
+/*
+ * Weight gradient of a projection whose input x was stored:
+ *   dW[n][k] = sum over rows t of dy[t][n] x[t][k]   (+ dW[n][k] where accumulate)
+ *   d_dy      x->rows x n_out, row distance ld_dy.
+ *   d_dw      n_out x x->cols, row distance ld_dw, f32, f16 or bf16.
+ * Products are exact and sums are in 32 bits: stored values and bf16
+ * gradients go into bf16 matrix instructions as they are; f16 and f32
+ * gradients go in as two and three bf16 terms that add up to them (two and
+ * three times the operations).
+ *   d_ws, ws_bytes  scratch of pc_q8_weight_grad_workspace_bytes (which may
+ *             be 0, then d_ws may be NULL), 16-byte aligned.
+ * x->rows == 0: dW = 0, or stays where accumulate.
+ */
+size_t pc_q8_weight_grad_workspace_bytes(size_t rows, size_t n_out, size_t n_in, int dy_dtype);
+pc_status pc_q8_weight_grad(const void *d_dy, int dy_dtype, size_t ld_dy, size_t n_out, const pc_q8 *x, void *d_dw,
+                            int dw_dtype, size_t ld_dw, int accumulate, void *d_ws, size_t ws_bytes, void *stream);
+
+/*
+ * Embedding lookup: out[t] = scale * table[token[t]].
+ *   d_tokens  n tokens, 4 or 8 bytes each (token_bytes), signed.
+ *   d_table   vocab x dim, row distance ld_table; pc_embed_q8 takes a stored
+ *             table (vocab = table->rows, dim = table->cols).
+ *   d_out     n x dim, row distance ld_out.
+ *   d_status  NULL, or one u32 that the caller has zeroed: a token outside
+ *             [0, vocab) sets it to PC_ERR_INVALID_ARG.  Its row of the
+ *             output is 0 either way.
+ */
+pc_status pc_embed(const void *d_tokens, int token_bytes, size_t n, const void *d_table, int table_dtype,
+                   size_t vocab, size_t dim, size_t ld_table, float scale, void *d_out, int out_dtype,
+                   size_t ld_out, uint32_t *d_status, void *stream);
+pc_status pc_embed_q8(const void *d_tokens, int token_bytes, size_t n, const pc_q8 *table, float scale, void *d_out,
+                      int out_dtype, size_t ld_out, uint32_t *d_status, void *stream);
+
+/*
+ * Gradient of the embedding table:
+ *   grad[v] = scale * sum over t with token[t] == v of dy[t]   (+ grad[v] where accumulate)
+ * Tokens are sorted first and each row is summed in the order of its tokens,
+ * in blocks of a size that depends on n alone, so the result has the same
+ * bits every time.  Rows without a token become 0 (stay, where accumulate).
+ * Tokens outside [0, vocab) and tokens equal to `padding` (-1: none) add
+ * nothing.
+ *   d_dy      n x dim, row distance ld_dy.
+ *   d_grad    vocab x dim, row distance ld_grad.
+ *   d_ws, ws_bytes  scratch of pc_embed_backward_workspace_bytes, 16-byte aligned.
+ * n below 2^31, vocab at most 2^31.
+ */
+size_t pc_embed_backward_workspace_bytes(size_t n, size_t dim, size_t vocab);
+pc_status pc_embed_backward(const void *d_dy, int dy_dtype, size_t ld_dy, const void *d_tokens, int token_bytes,
+                            size_t n, size_t dim, size_t vocab, int64_t padding, float scale, void *d_grad,
+                            int grad_dtype, size_t ld_grad, int accumulate, void *d_ws, size_t ws_bytes,
+                            void *stream);
 
 #ifdef __cplusplus
 }

@@ -28,6 +28,8 @@ EXPORTS = [
     "pc_num_chunks", "pc_num_substreams", "pc_max_payload_words", "pc_encode_workspace_bytes",
     "pc_encode", "pc_encode_noalloc", "pc_encode_set_wait_limit", "pc_decode", "pc_decode_qlc", "pc_histogram",
     "pc_traffic_probe",
+    "pc_q8_store", "pc_q8_load", "pc_q8_glu_backward", "pc_q8_weight_grad_workspace_bytes", "pc_q8_weight_grad",
+    "pc_embed", "pc_embed_q8", "pc_embed_backward_workspace_bytes", "pc_embed_backward",
 ]
 
 
@@ -35,6 +37,12 @@ class PcError(RuntimeError):
     def __init__(self, status, what):
         super().__init__("%s: %s (status %d)" % (what, status_string(status), status))
         self.status = status
+
+
+class StoredArg(C.Structure):
+    """The header's pc_q8: a stored tensor as an argument."""
+    _fields_ = [("sym", C.c_void_p), ("scale", C.c_void_p), ("rows", C.c_uint64), ("cols", C.c_uint64),
+                ("ld_sym", C.c_uint64), ("ld_scale", C.c_uint64), ("format", C.c_int32), ("reserved", C.c_int32)]
 
 
 def _load():
@@ -61,9 +69,23 @@ def _load():
     lib.pc_decode_qlc.argtypes = [p, p, sz, p, p, p, sz, sz, p, p, p]
     lib.pc_histogram.argtypes = [p, sz, p, p]
     lib.pc_traffic_probe.argtypes = [p, p, sz, p]
+    q8, i64, f32 = C.POINTER(StoredArg), C.c_int64, C.c_float
+    lib.pc_q8_store.argtypes = [p, i, sz, sz, sz, i, p, p, p, p]
+    lib.pc_q8_load.argtypes = [q8, p, i, sz, p]
+    lib.pc_q8_glu_backward.argtypes = [p, i, sz, q8, q8, i, p, sz, p, sz, p, sz, p]
+    lib.pc_q8_weight_grad_workspace_bytes.argtypes = [sz, sz, sz, i]
+    lib.pc_q8_weight_grad_workspace_bytes.restype = sz
+    lib.pc_q8_weight_grad.argtypes = [p, i, sz, sz, q8, p, i, sz, i, p, sz, p]
+    lib.pc_embed.argtypes = [p, i, sz, p, i, sz, sz, sz, f32, p, i, sz, p, p]
+    lib.pc_embed_q8.argtypes = [p, i, sz, q8, f32, p, i, sz, p, p]
+    lib.pc_embed_backward_workspace_bytes.argtypes = [sz, sz, sz]
+    lib.pc_embed_backward_workspace_bytes.restype = sz
+    lib.pc_embed_backward.argtypes = [p, i, sz, p, i, sz, sz, sz, i64, f32, p, i, sz, i, p, sz, p]
     for f in ("pc_codebook_build", "pc_codebook_validate", "pc_qlc_optimal_bits", "pc_codebook_fit",
               "pc_shard_code_lengths", "pc_encode", "pc_encode_noalloc",
-              "pc_decode", "pc_decode_qlc", "pc_histogram", "pc_traffic_probe"):
+              "pc_decode", "pc_decode_qlc", "pc_histogram", "pc_traffic_probe",
+              "pc_q8_store", "pc_q8_load", "pc_q8_glu_backward", "pc_q8_weight_grad",
+              "pc_embed", "pc_embed_q8", "pc_embed_backward"):
         getattr(lib, f).restype = i
     return lib
 

@@ -108,4 +108,27 @@ hipError_t launch_decode(int mode, const pc_codebook *cb, const uint32_t *payloa
 
 hipError_t launch_histogram(const uint8_t *in, uint64_t n, uint64_t *counts, hipStream_t stream);
 
+hipError_t launch_q8_store(const void *x, int dtype, uint64_t rows, uint64_t cols, uint64_t ldx, int format,
+                           uint8_t *sym, uint8_t *scale, uint64_t *counts, hipStream_t stream);
+
+hipError_t launch_q8_load(const pc_q8 *q, void *out, int dtype, uint64_t ld_out, hipStream_t stream);
+
+hipError_t launch_q8_glu_backward(const void *dh, int dtype, uint64_t ld_dh, const pc_q8 *gate, const pc_q8 *up,
+                                  int act, void *d_gate, uint64_t ld_gate, void *d_up, uint64_t ld_up, void *h,
+                                  uint64_t ld_h, hipStream_t stream);
+
+uint64_t wgrad_workspace(uint64_t t, uint64_t n, uint64_t k, int dy_dtype);
+hipError_t launch_q8_weight_grad(const void *dy, int dtype, uint64_t ld_dy, uint64_t n_out, const pc_q8 *x, void *dw,
+                                 int dw_dtype, uint64_t ld_dw, bool accumulate, void *ws, hipStream_t stream);
+
+// kind: a pc_dtype, or 4 + a pc_q8_format for a stored table (then with codes).
+hipError_t launch_embed(const void *tokens, int token_bytes, uint64_t n, const void *table, const uint8_t *codes,
+                        int kind, uint64_t vocab, uint64_t dim, uint64_t ld_table, uint64_t ld_codes, float scale,
+                        void *out, int out_dtype, uint64_t ld_out, uint32_t *status, hipStream_t stream);
+
+uint64_t embed_backward_workspace(uint64_t n, uint64_t dim, uint64_t vocab);
+hipError_t launch_embed_backward(const void *dy, int dtype, uint64_t ld_dy, const void *tokens, int token_bytes,
+                                 uint32_t n, uint64_t dim, uint64_t vocab, int64_t padding, float scale, void *grad,
+                                 int grad_dtype, uint64_t ld_grad, bool accumulate, void *ws, hipStream_t stream);
+
 }  // namespace pc
