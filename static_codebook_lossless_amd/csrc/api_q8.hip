@@ -9,6 +9,7 @@ namespace {
 // 512 units of 8 columns.
 constexpr uint64_t kMaxGroups = (1ull << 24) - 1;
 constexpr uint64_t kMaxWidth = 1ull << 31;
+constexpr uint64_t kMaxDistance = 1ull << 24;  // weight gradient: offsets inside a tile of 64 rows stay below 2^32 bytes
 constexpr uint64_t kMaxElements = 1ull << 47;  // beyond any memory; keeps sizes below 64 bits
 
 bool is_dtype(int d) { return d == PC_F32 || d == PC_F16 || d == PC_BF16; }
@@ -98,6 +99,8 @@ pc_status pc_q8_weight_grad(const void *d_dy, int dy_dtype, size_t ld_dy, size_t
     if (rows && (!plain_ok(d_dy, dy_dtype, n_out, ld_dy) || !stored_ok(x))) return PC_ERR_INVALID_ARG;
     if (!size_ok(n_out, n_in) || !size_ok(rows, n_out) || !size_ok(rows, n_in) || !span_ok(n_out, ld_dw) ||
         (rows && (!span_ok(rows, ld_dy) || !span_ok(rows, x->ld_sym) || !span_ok(rows, x->ld_scale))))
+        return PC_ERR_UNSUPPORTED;
+    if (rows && (ld_dy >= kMaxDistance || x->ld_sym >= kMaxDistance || x->ld_scale >= kMaxDistance))
         return PC_ERR_UNSUPPORTED;
     const size_t need = pc_q8_weight_grad_workspace_bytes(rows, n_out, n_in, dy_dtype);
     if (need) {

@@ -18,7 +18,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr uint32_t kThreads = 256;
-constexpr uint32_t kStep = 64;  // rows t of one LDS tile
+constexpr uint32_t kStep = 64;               // rows t of one LDS tile
+constexpr uint32_t kBlocks = kStep / 8;      // blocks of 8 rows in it
 
 // dy as sums of bf16 terms: bf16 is its own, f16 (11 bits) needs two of 8
 // bits, f32 (24 bits) three.
@@ -43,76 +44,102 @@ __device__ __forceinline__ uint32_t term_bits(float v, uint32_t which) {
     return as_u32(t);
 }
 
-template <int DT> struct RawUnit { u32x4 w; };
-template <> struct RawUnit<PC_F32> { u32x4 w, w2; };
-
-template <int DT>
-__device__ __forceinline__ void load_raw(const typename Plain<DT>::type *p, uint32_t n, RawUnit<DT> &r) {
-    if (n == kUnit) {
-        if constexpr (DT == PC_F32) {
-            r.w = *reinterpret_cast<const u32x4_any4 *>(p);
-            r.w2 = *reinterpret_cast<const u32x4_any4 *>(p + 4);
-        } else {
-            r.w = *reinterpret_cast<const u32x4_any2 *>(p);
-        }
-        return;
-    }
-    if constexpr (DT == PC_F32) {
-#pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) {
-            r.w[i] = i < n ? as_u32(p[i]) : 0u;
-            r.w2[i] = 4 + i < n ? as_u32(p[4 + i]) : 0u;
-        }
-    } else {
-        const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
-#pragma unroll
-        for (uint32_t i = 0; i < 4; ++i)
-            r.w[i] = (2 * i < n ? q[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)q[2 * i + 1] << 16 : 0u);
-    }
+// Memory as the hardware's bounds-checked buffer: a load that starts at or
+// past `bytes` reads 0.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ __forceinline__ Buffer make_buffer(const void *p, uint64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)(uint32_t)min(bytes, (uint64_t)0xFFFFFFFFu),
+                                             0x00020000);
 }
 
-// The four words (bf16 pairs) of a row's 8 columns.
-template <int DT>
-__device__ __forceinline__ void to_bf16(const RawUnit<DT> &r, uint32_t which, uint32_t w[4]) {
-    if constexpr (DT == PC_BF16) {
+// A block of 8 rows of 8 columns as loaded: rows of 8 elements of dy, or of
+// 8 symbols of x with the rows' scale codes.
+template <int DT> struct RawDy {
+    static constexpr uint32_t kWords = DT == PC_F32 ? 2 : 1;
+    u32x4 w[8][kWords];
+
+    __device__ __forceinline__ void load(Buffer b, const uint32_t at[8]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = r.w[i];
-    } else {
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float a, b;
-            if constexpr (DT == PC_F16) {
-                const uint32_t u = r.w[i];
-                const f16x2 h = __builtin_bit_cast(f16x2, u);
-                a = (float)h[0];
-                b = (float)h[1];
+            for (uint32_t k = 0; k < kWords; ++k) w[i][k] = __builtin_amdgcn_raw_buffer_load_b128(b, at[i] + 16 * k, 0, 0);
+    }
+    // the first n elements of row i, each by itself
+    __device__ __forceinline__ void load_single(int i, Buffer b, uint32_t at, uint32_t n) {
+#pragma unroll
+        for (uint32_t c = 0; c < 8; ++c) {
+            if constexpr (DT == PC_F32) {
+                w[i][c / 4][c % 4] = c < n ? __builtin_amdgcn_raw_buffer_load_b32(b, at + 4 * c, 0, 0) : 0u;
             } else {
-                a = as_f32(i < 2 ? r.w[2 * (i % 2)] : r.w2[2 * (i % 2)]);
-                b = as_f32(i < 2 ? r.w[2 * (i % 2) + 1] : r.w2[2 * (i % 2) + 1]);
+                const uint32_t e = c < n ? (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b, at + 2 * c, 0, 0) : 0u;
+                w[i][0][c / 2] = c % 2 ? w[i][0][c / 2] | e << 16 : e;
             }
-            w[i] = __builtin_amdgcn_perm(term_bits(b, which), term_bits(a, which), 0x07060302u);
         }
     }
-}
-
-template <int FMT>
-__device__ __forceinline__ void to_bf16(u32x2 s, float scale, uint32_t w[4]) {
-    if constexpr (FMT == PC_Q8_E4M3) {
-        w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(s[0], scale, false));
-        w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(s[0], scale, true));
-        w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(s[1], scale, false));
-        w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(s[1], scale, true));
-    } else {
-        float v[8];
-        unit_values<FMT>(s, scale, v);
+    // bf16 pairs of row i
+    __device__ __forceinline__ void words(int i, uint32_t which, uint32_t out[4]) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_perm(as_u32(v[2 * i + 1]), as_u32(v[2 * i]), 0x07060302u);
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (DT == PC_BF16) {
+                out[k] = w[i][0][k];
+            } else {
+                float a, b;
+                if constexpr (DT == PC_F16) {
+                    const uint32_t u = w[i][0][k];
+                    const f16x2 h = __builtin_bit_cast(f16x2, u);
+                    a = (float)h[0];
+                    b = (float)h[1];
+                } else {
+                    a = as_f32(w[i][(2 * k) / 4][(2 * k) % 4]);
+                    b = as_f32(w[i][(2 * k) / 4][(2 * k) % 4 + 1]);
+                }
+                out[k] = __builtin_amdgcn_perm(term_bits(b, which), term_bits(a, which), 0x07060302u);
+            }
+        }
     }
-}
+};
 
-// 8 rows of 8 columns (bf16 pairs along the columns) to eight 16-byte pieces
-// of 8 rows, written to LDS `distance` pieces apart.
-__device__ __forceinline__ void put_transposed(const uint32_t w[8][4], u32x4 *to, uint32_t distance) {
+template <int FMT> struct RawX {
+    u32x2 w[8];
+    uint32_t code[8];
+
+    __device__ __forceinline__ void load(Buffer b, const uint32_t at[8], Buffer codes, const uint32_t code_at[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            w[i] = __builtin_amdgcn_raw_buffer_load_b64(b, at[i], 0, 0);
+            code[i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(codes, code_at[i], 0, 0);
+        }
+    }
+    __device__ __forceinline__ void load_single(int i, Buffer b, uint32_t at, uint32_t n) {
+        w[i] = u32x2{0, 0};
+#pragma unroll
+        for (uint32_t c = 0; c < 8; ++c)
+            if (c < n) w[i][c / 4] |= (uint32_t)(uint8_t)__builtin_amdgcn_raw_buffer_load_b8(b, at + c, 0, 0) << (8 * (c % 4));
+    }
+    __device__ __forceinline__ void words(int i, uint32_t, uint32_t out[4]) const {
+        const float s = scale_of(code[i]);
+        if constexpr (FMT == PC_Q8_E4M3) {
+            out[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i][0], s, false));
+            out[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i][0], s, true));
+            out[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i][1], s, false));
+            out[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i][1], s, true));
+        } else {
+            float v[8];
+            unit_values<FMT>(w[i], s, v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                out[k] = __builtin_amdgcn_perm(as_u32(v[2 * k + 1]), as_u32(v[2 * k]), 0x07060302u);
+        }
+    }
+};
+
+// A block in LDS: eight 16-byte pieces, one for each column with its 8 rows,
+// `distance` pieces apart.
+template <class RAW>
+__device__ __forceinline__ void put_transposed(const RAW &r, uint32_t which, u32x4 *to, uint32_t distance) {
+    uint32_t w[8][4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.words(i, which, w[i]);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         u32x4 even, odd;
@@ -126,37 +153,104 @@ __device__ __forceinline__ void put_transposed(const uint32_t w[8][4], u32x4 *to
     }
 }
 
-// Column of the piece at place p of a tile of B columns: pieces are placed so
-// that neighbouring lanes, which hold neighbouring blocks of 8 columns, write
-// neighbouring pieces.
-template <uint32_t B>
-__device__ __forceinline__ uint32_t column_at(uint32_t p) {
-    return (p % (B / 8)) * 8 + p / (B / 8);
+// Where a tile of B columns keeps its pieces: block l of 8 columns is one
+// lane's, and the pieces of its column c lie at c * (B / 8) + l, so that
+// neighbouring lanes write, and later read, neighbouring pieces.  A wave with
+// F fragments of 32 columns takes the columns c of its share of every block;
+// its fragment j, lane r has column c = column_in_block(j, r) of block r % (B / 8),
+// so that a lane's fragments are neighbouring columns of the result.
+template <uint32_t B, uint32_t F>
+__device__ __forceinline__ uint32_t column_in_block(uint32_t wave, uint32_t j, uint32_t r) {
+    return wave * (F * 256 / B) + r / (B / 8) * F + j;
 }
 
 struct Shape {
-    uint64_t t, n, k;       // rows, n_out, n_in
-    uint64_t ld_dy, ld_out;
-    uint64_t slice;         // rows of one slice of t (a multiple of kStep)
+    uint64_t t, n, k;  // rows, n_out, n_in
+    uint64_t ld_dy, ld_sym, ld_scale, ld_out;
+    uint32_t slice;    // LDS tiles of one slice of t
     uint32_t tiles_n, tiles_k;
 };
 
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 template <int DT, int FMT, int ODT, uint32_t WN, uint32_t WK, uint32_t FN, uint32_t FK>
-__global__ __launch_bounds__(kThreads) void wgrad_kernel(const typename Plain<DT>::type *__restrict__ dy,
-                                                         const uint8_t *__restrict__ sym,
-                                                         const uint8_t *__restrict__ scale, uint64_t ld_sym,
-                                                         uint64_t ld_scale, Shape s,
-                                                         typename Plain<ODT>::type *__restrict__ out, uint32_t add) {
-    constexpr uint32_t BN = WN * FN * 32, BK = WK * FK * 32;
-    static_assert(WN * WK * kWave == kThreads, "waves");
-    __shared__ u32x4 ly[kStep / 8 * BN];
-    __shared__ u32x4 lx[kStep / 8 * BK];
-    const uint32_t tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+__global__ __launch_bounds__(WN *WK *kWave, 1) void wgrad_kernel(const typename Plain<DT>::type *__restrict__ dy,
+                                                                 const uint8_t *__restrict__ sym,
+                                                                 const uint8_t *__restrict__ scale, Shape s,
+                                                                 typename Plain<ODT>::type *__restrict__ out,
+                                                                 uint32_t add) {
+    constexpr uint32_t BN = WN * FN * 32, BK = WK * FK * 32, NT = WN * WK * kWave;
+    constexpr uint32_t kElem = sizeof(typename Plain<DT>::type);
+    // blocks of the two tiles: one of each for every lane, or one for every lane of either half
+    constexpr bool kBoth = kBlocks * BN / 8 == NT && kBlocks * BK / 8 == NT;
+    static_assert(kBoth || (kBlocks * BN / 8 == NT / 2 && kBlocks * BK / 8 == NT / 2), "blocks");
+    __shared__ u32x4 ly[2][kBlocks * BN];
+    __shared__ u32x4 lx[2][kBlocks * BK];
+    const uint32_t tid = threadIdx.x, lane = tid % kWave, wave = uniform(tid / kWave);
     const uint32_t wn = wave / WK, wk = wave % WK;
-    const uint32_t tile = blockIdx.x;
-    const uint64_t n0 = (uint64_t)(tile / s.tiles_k) * BN, k0 = (uint64_t)(tile % s.tiles_k) * BK;
-    const uint64_t t_begin = (uint64_t)blockIdx.y * s.slice, t_end = min(s.t, t_begin + s.slice);
-    out += (uint64_t)blockIdx.y * s.n * s.k;  // a slice's own partial sums (one slice: the output)
+    const uint64_t n0 = (uint64_t)(blockIdx.x / s.tiles_k) * BN, k0 = (uint64_t)(blockIdx.x % s.tiles_k) * BK;
+    const uint32_t all = (uint32_t)((s.t + kStep - 1) / kStep);
+    const uint32_t first = min(all, blockIdx.y * s.slice), tiles = min(all - first, s.slice);
+    const uint32_t steps = tiles * kTerms<DT>;
+    if constexpr (ODT == PC_F32) out += (uint64_t)blockIdx.y * s.n * s.k;  // a slice's partial sums (one slice: the output)
+
+    const bool has_dy = kBoth || wave < WN * WK / 2, has_x = kBoth || !has_dy;
+    const uint32_t b = kBoth ? tid : tid % (NT / 2);
+    const uint32_t yl = b % (BN / 8), yt = b / (BN / 8), xl = b % (BK / 8), xt = b / (BK / 8);
+    uint32_t y_at[8], x_at[8], c_at[8];
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) {
+        y_at[i] = (yt * 8 + i) * (uint32_t)s.ld_dy * kElem + yl * 8 * kElem;
+        x_at[i] = (xt * 8 + i) * (uint32_t)s.ld_sym + xl * 8;
+        c_at[i] = (xt * 8 + i) * (uint32_t)s.ld_scale + xl / kUnitsPerGroup;
+    }
+    RawDy<DT> ry;
+    RawX<FMT> rx;
+
+    // Loads tile i (past the last: zeros) into registers.
+    auto load = [&](uint32_t i) {
+        const uint64_t t0 = (uint64_t)(first + (kTerms<DT> == 1 ? i : i % tiles)) * kStep;
+        const uint64_t rows = i < steps ? s.t - t0 : 0;  // rows from t0 to the tensor's end
+        const bool near = rows && rows < kStep + 8;
+        if (has_dy) {
+            const uint64_t bytes = rows ? ((rows - 1) * s.ld_dy + (s.n - n0)) * kElem : 0;
+            const Buffer buf = make_buffer(dy + (rows ? t0 * s.ld_dy + n0 : 0), bytes);
+            ry.load(buf, y_at);
+            // a block that sticks out of the tensor's last row: the load may have
+            // dropped the elements that are in it
+            const uint64_t c = n0 + yl * 8;
+            if (near && n0 + BN > s.n && c < s.n && c + 8 > s.n) {
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (y_at[r] < bytes && y_at[r] + 8 * kElem > bytes)
+                        ry.load_single(r, buf, y_at[r], (uint32_t)(s.n - c));
+            }
+        }
+        if (has_x) {
+            const uint64_t bytes = rows ? (rows - 1) * s.ld_sym + (s.k - k0) : 0;
+            const Buffer buf = make_buffer(sym + (rows ? t0 * s.ld_sym + k0 : 0), bytes);
+            const uint64_t groups = (s.k + kGroup - 1) / kGroup - k0 / kGroup;
+            const Buffer codes = make_buffer(scale + (rows ? t0 * s.ld_scale + k0 / kGroup : 0),
+                                             rows ? (rows - 1) * s.ld_scale + groups : 0);
+            rx.load(buf, x_at, codes, c_at);
+            const uint64_t c = k0 + xl * 8;
+            if (near && k0 + BK > s.k && c < s.k && c + 8 > s.k) {
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (x_at[r] < bytes && x_at[r] + 8 > bytes) rx.load_single(r, buf, x_at[r], (uint32_t)(s.k - c));
+            }
+        }
+    };
+    auto put_dy = [&](uint32_t i) {
+        if (has_dy) put_transposed(ry, kTerms<DT> == 1 ? 0 : i / tiles, ly[i & 1] + yt * BN + yl, BN / 8);
+    };
+    auto put_x = [&](uint32_t i) {
+        if (has_x) put_transposed(rx, 0, lx[i & 1] + xt * BK + xl, BK / 8);
+    };
 
     f32x16 acc[FN][FK];
 #pragma unroll
@@ -164,75 +258,68 @@ __global__ __launch_bounds__(kThreads) void wgrad_kernel(const typename Plain<DT
 #pragma unroll
         for (uint32_t j = 0; j < FK; ++j) acc[i][j] = f32x16{0};
 
-    for (uint32_t which = 0; which < kTerms<DT>; ++which) {
-        for (uint64_t t0 = t_begin; t0 < t_end; t0 += kStep) {
-            __syncthreads();
-            for (uint32_t b = tid; b < kStep / 8 * BN / 8; b += kThreads) {
-                const uint32_t tb = b / (BN / 8), l = b % (BN / 8);
-                const uint64_t c = n0 + l * 8;
-                const uint32_t n = c < s.n ? (uint32_t)min((uint64_t)8, s.n - c) : 0;
-                uint32_t w[8][4];
+    if (steps) {
+        const uint32_t r = lane % 32, half = lane / 32;
+        uint32_t a_at[FN], b_at[FK];
 #pragma unroll
-                for (uint32_t i = 0; i < 8; ++i) {
-                    RawUnit<DT> r = {};
-                    const uint64_t t = t0 + tb * 8 + i;
-                    if (n && t < t_end) load_raw<DT>(dy + t * s.ld_dy + c, n, r);
-                    to_bf16<DT>(r, which, w[i]);
-                }
-                put_transposed(w, ly + tb * BN + l, BN / 8);
-            }
-            for (uint32_t b = tid; b < kStep / 8 * BK / 8; b += kThreads) {
-                const uint32_t tb = b / (BK / 8), l = b % (BK / 8);
-                const uint64_t c = k0 + l * 8;
-                const uint32_t n = c < s.k ? (uint32_t)min((uint64_t)8, s.k - c) : 0;
-                uint32_t w[8][4];
+        for (uint32_t i = 0; i < FN; ++i)
+            a_at[i] = half * BN + column_in_block<BN, FN>(wn, i, r) * (BN / 8) + r % (BN / 8);
 #pragma unroll
-                for (uint32_t i = 0; i < 8; ++i) {
-                    u32x2 q = {0, 0};
-                    uint32_t code = 127;
-                    const uint64_t t = t0 + tb * 8 + i;
-                    if (n && t < t_end) {
-                        q = load_symbols(sym + t * ld_sym + c, n);
-                        code = scale[t * ld_scale + c / kGroup];
-                    }
-                    to_bf16<FMT>(q, scale_of(code), w[i]);
-                }
-                put_transposed(w, lx + tb * BK + l, BK / 8);
-            }
-            __syncthreads();
+        for (uint32_t j = 0; j < FK; ++j)
+            b_at[j] = half * BK + column_in_block<BK, FK>(wk, j, r) * (BK / 8) + r % (BK / 8);
+        bf16x8 fa[2][FN], fb[2][FK];
+        auto read = [&](uint32_t which, uint32_t buf, uint32_t kk) {
 #pragma unroll
-            for (uint32_t kk = 0; kk < kStep / 16; ++kk) {
-                bf16x8 a[FN], b[FK];
-                const uint32_t tb = kk * 2 + lane / 32;
+            for (uint32_t i = 0; i < FN; ++i) fa[which][i] = __builtin_bit_cast(bf16x8, ly[buf][a_at[i] + kk * 2 * BN]);
 #pragma unroll
-                for (uint32_t i = 0; i < FN; ++i)
-                    a[i] = __builtin_bit_cast(bf16x8, ly[tb * BN + (wn * FN + i) * 32 + lane % 32]);
+            for (uint32_t j = 0; j < FK; ++j) fb[which][j] = __builtin_bit_cast(bf16x8, lx[buf][b_at[j] + kk * 2 * BK]);
+        };
+        auto multiply = [&](uint32_t which) {
+#pragma unroll
+            for (uint32_t i = 0; i < FN; ++i)
 #pragma unroll
                 for (uint32_t j = 0; j < FK; ++j)
-                    b[j] = __builtin_bit_cast(bf16x8, lx[tb * BK + (wk * FK + j) * 32 + lane % 32]);
-#pragma unroll
-                for (uint32_t i = 0; i < FN; ++i)
-#pragma unroll
-                    for (uint32_t j = 0; j < FK; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
-            }
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[which][i], fb[which][j], acc[i][j], 0, 0, 0);
+        };
+        load(0);
+        put_dy(0);
+        put_x(0);
+        load(1);
+        lds_barrier();
+        read(0, 0, 0);
+        for (uint32_t i = 0; i < steps; ++i) {
+            const uint32_t buf = i & 1;
+            read(1, buf, 1);
+            put_dy(i + 1);
+            multiply(0);
+            read(0, buf, 2);
+            put_x(i + 1);
+            multiply(1);
+            read(1, buf, 3);
+            load(i + 2);
+            multiply(0);
+            lds_barrier();
+            read(0, buf ^ 1, 0);
+            multiply(1);
         }
     }
+
+    const uint32_t r0 = lane % 32;
+    const uint64_t k = k0 + r0 % (BK / 8) * 8 + column_in_block<BK, FK>(wk, 0, r0);
 #pragma unroll
     for (uint32_t i = 0; i < FN; ++i)
 #pragma unroll
         for (uint32_t v = 0; v < 16; ++v) {
             const uint32_t r = v / 4 * 8 + lane / 32 * 4 + v % 4;
-            const uint64_t n = n0 + column_at<BN>((wn * FN + i) * 32 + r);
+            const uint64_t n = n0 + r % (BN / 8) * 8 + column_in_block<BN, FN>(wn, i, r);
             if (n >= s.n) continue;
+            typename Plain<ODT>::type *p = out + n * s.ld_out + k;
 #pragma unroll
-            for (uint32_t j = 0; j < FK; ++j) {
-                const uint64_t k = k0 + column_at<BK>((wk * FK + j) * 32 + lane % 32);
-                if (k >= s.k) continue;
-                typename Plain<ODT>::type *p = out + n * s.ld_out + k;
-                const float old = add ? widen(*p) : 0.0f;
-                *p = (typename Plain<ODT>::type)(acc[i][j][v] + old);
-            }
+            for (uint32_t j = 0; j < FK; ++j)
+                if (k + j < s.k) {
+                    const float old = add ? widen(p[j]) : 0.0f;
+                    p[j] = (typename Plain<ODT>::type)(acc[i][j][v] + old);
+                }
         }
 }
 
@@ -249,50 +336,64 @@ __global__ __launch_bounds__(kThreads) void join_kernel(const float *__restrict_
     *p = (typename Plain<ODT>::type)(v + (add ? widen(*p) : 0.0f));
 }
 
-constexpr uint32_t kTileN = 128, kTileK = 128;
+// Tile sides: 256 (a wave's 128 x 128 part reads the least from LDS for each
+// product), or 128 where that leaves workgroup slots empty.
+uint64_t tiles_of(uint64_t n, uint64_t k, uint32_t side) { return ((n + side - 1) / side) * ((k + side - 1) / side); }
 
-uint32_t slices_of(uint64_t t, uint64_t n, uint64_t k) {
-    const uint64_t tiles = ((n + kTileN - 1) / kTileN) * ((k + kTileK - 1) / kTileK);
+struct Plan {
+    uint32_t side, slices, slice;
+};
+
+Plan plan_of(uint64_t t, uint64_t n, uint64_t k) {
+    Plan p;
     const uint64_t steps = (t + kStep - 1) / kStep;
-    if (tiles >= 256 || steps < 8) return 1;
-    return (uint32_t)std::min<uint64_t>(512 / tiles, steps / 4);
+    p.side = tiles_of(n, k, 256) >= 192 ? 256 : 128;
+    const uint64_t tiles = tiles_of(n, k, p.side);
+    p.slices = 1;
+    if (tiles < 256 && steps >= 8) p.slices = (uint32_t)std::min<uint64_t>(512 / tiles, steps / 4);
+    p.slice = (uint32_t)((steps + p.slices - 1) / p.slices);
+    return p;
 }
 
 }  // namespace
 
 uint64_t wgrad_workspace(uint64_t t, uint64_t n, uint64_t k, int) {
-    const uint32_t slices = slices_of(t, n, k);
-    return slices > 1 ? (uint64_t)slices * n * k * 4 : 0;
+    const Plan p = plan_of(t, n, k);
+    return p.slices > 1 ? (uint64_t)p.slices * n * k * 4 : 0;
 }
 
 hipError_t launch_q8_weight_grad(const void *dy, int dtype, uint64_t ld_dy, uint64_t n_out, const pc_q8 *x, void *dw,
                                  int dw_dtype, uint64_t ld_dw, bool accumulate, void *ws, hipStream_t stream) {
     const uint64_t t = x->rows, n = n_out, k = x->cols;
-    const uint32_t slices = slices_of(t, n, k);
-    Shape s = {t, n, k, ld_dy, slices > 1 ? k : ld_dw, 0, (uint32_t)((n + kTileN - 1) / kTileN),
-               (uint32_t)((k + kTileK - 1) / kTileK)};
-    const uint64_t steps = (t + kStep - 1) / kStep;
-    s.slice = (steps + slices - 1) / slices * kStep;
-    const dim3 grid(s.tiles_n * s.tiles_k, slices);
+    const Plan p = plan_of(t, n, k);
+    const bool split = p.slices > 1;
+    const Shape s = {t, n, k, ld_dy, x->ld_sym, x->ld_scale, split ? k : ld_dw, p.slice,
+                     (uint32_t)((n + p.side - 1) / p.side), (uint32_t)((k + p.side - 1) / p.side)};
+    const dim3 grid(s.tiles_n * s.tiles_k, p.slices);
     with_dtype(dtype, [&](auto d) {
         constexpr int DT = decltype(d)::value;
-        with_dtype(slices > 1 ? (int)PC_F32 : dw_dtype, [&](auto o) {
+        with_dtype(split ? (int)PC_F32 : dw_dtype, [&](auto o) {
             constexpr int ODT = decltype(o)::value;
             auto launch = [&](auto kern) {
                 hipLaunchKernelGGL(kern, grid, dim3(kThreads), 0, stream,
-                                   static_cast<const typename Plain<DT>::type *>(dy), x->sym, x->scale, x->ld_sym,
-                                   x->ld_scale, s, static_cast<typename Plain<ODT>::type *>(slices > 1 ? ws : dw),
-                                   (uint32_t)(accumulate && slices == 1));
+                                   static_cast<const typename Plain<DT>::type *>(dy), x->sym, x->scale, s,
+                                   static_cast<typename Plain<ODT>::type *>(split ? ws : dw),
+                                   (uint32_t)(accumulate && !split));
             };
-            x->format == PC_Q8_E4M3 ? launch(wgrad_kernel<DT, PC_Q8_E4M3, ODT, 2, 2, 2, 2>)
-                                    : launch(wgrad_kernel<DT, PC_Q8_INT8, ODT, 2, 2, 2, 2>);
+            auto by_format = [&](auto f) {
+                constexpr int FMT = decltype(f)::value;
+                p.side == 256 ? launch(wgrad_kernel<DT, FMT, ODT, 2, 2, 4, 4>)
+                              : launch(wgrad_kernel<DT, FMT, ODT, 2, 2, 2, 2>);
+            };
+            if (x->format == PC_Q8_E4M3) by_format(std::integral_constant<int, PC_Q8_E4M3>());
+            else by_format(std::integral_constant<int, PC_Q8_INT8>());
         });
     });
-    if (slices > 1)
+    if (split)
         with_dtype(dw_dtype, [&](auto o) {
             constexpr int ODT = decltype(o)::value;
             hipLaunchKernelGGL(join_kernel<ODT>, dim3((uint32_t)((n * k + kThreads - 1) / kThreads)), dim3(kThreads), 0,
-                               stream, static_cast<const float *>(ws), slices, n, k, ld_dw,
+                               stream, static_cast<const float *>(ws), p.slices, n, k, ld_dw,
                                static_cast<typename Plain<ODT>::type *>(dw), (uint32_t)accumulate);
         });
     return hipGetLastError();
