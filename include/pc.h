@@ -455,13 +455,14 @@ pc_status pc_embed_q8(const void *d_tokens, int token_bytes, size_t n, const pc_
  * Gradient of the embedding table:
  *   grad[v] = scale * sum over t with token[t] == v of dy[t]   (+ grad[v] where accumulate)
  * Tokens are sorted first and each row is summed in the order of its tokens,
- * in blocks of a size that depends on n alone, so the result has the same
+ * in blocks whose sizes depend on the call's sizes alone, so the result has the same
  * bits every time.  Rows without a token become 0 (stay, where accumulate).
  * Tokens outside [0, vocab) and tokens equal to `padding` (-1: none) add
  * nothing.
  *   d_dy      n x dim, row distance ld_dy.
  *   d_grad    vocab x dim, row distance ld_grad.
- *   d_ws, ws_bytes  scratch of pc_embed_backward_workspace_bytes, 16-byte aligned.
+ *   d_ws, ws_bytes  scratch of pc_embed_backward_workspace_bytes (0 for few
+ *             tokens, then d_ws may be NULL), 16-byte aligned.
  * n below 2^31, vocab at most 2^31.
  */
 size_t pc_embed_backward_workspace_bytes(size_t n, size_t dim, size_t vocab);

@@ -162,10 +162,13 @@ pc_status pc_embed_backward(const void *d_dy, int dy_dtype, size_t ld_dy, const 
         return PC_ERR_INVALID_ARG;
     // the sums take a wave for every 32 sorted tokens and 512 columns, the zeros one for every row
     if (n >= kMaxWidth || vocab > kMaxWidth || !size_ok(n, dim) || !size_ok(vocab, dim) || !span_ok(vocab, ld_grad) ||
-        (n && !span_ok(n, ld_dy)) || ((n + 31) / 32 * ((dim + 511) / 512) + vocab) / 4 >= kMaxGroups)
+        (n && !span_ok(n, ld_dy)) || (n + 31) / 32 * ((dim + 511) / 512) + vocab / 4 >= kMaxGroups || (dim + 511) / 512 > 65535)
         return PC_ERR_UNSUPPORTED;
-    if (!d_ws || (reinterpret_cast<uintptr_t>(d_ws) & 15)) return PC_ERR_INVALID_ARG;
-    if (ws_bytes < pc_embed_backward_workspace_bytes(n, dim, vocab)) return PC_ERR_CAPACITY;
+    const size_t need = pc_embed_backward_workspace_bytes(n, dim, vocab);
+    if (need) {
+        if (!d_ws || (reinterpret_cast<uintptr_t>(d_ws) & 15)) return PC_ERR_INVALID_ARG;
+        if (ws_bytes < need) return PC_ERR_CAPACITY;
+    }
     return map_hip(pc::launch_embed_backward(d_dy, dy_dtype, ld_dy, d_tokens, token_bytes, (uint32_t)n, dim, vocab,
                                              padding, scale, d_grad, grad_dtype, ld_grad, accumulate != 0, d_ws,
                                              static_cast<hipStream_t>(stream)));

@@ -73,9 +73,255 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(const void *__restrict_
 // gradient: sort the tokens, sum the rows of dy in that order
 // ---------------------------------------------------------------------------
 
-// Workspace: start[vocab + 1] (first sorted place of each token), key[n] and
-// source[n] (token and row of dy at each sorted place), partial sums of the
-// runs that cross a block's end.
+// A wave holds a slab of 512 columns of a row, a lane 4 of either half of it:
+// every load and store of the wave is then one piece of memory without gaps,
+// in each of the types.
+constexpr uint32_t kSlab = 512;
+constexpr uint32_t kAhead = 8;  // rows of dy in flight in a lane
+
+// WHOLE: the width is a multiple of 4.
+template <bool WHOLE> struct Columns {
+    uint64_t first[2], last;  // the lane's first column of either four; the row's last
+    uint32_t n[2];            // how many of each four are inside
+    __device__ __forceinline__ Columns(uint64_t slab, uint32_t lane, uint64_t dim) : last(dim - 1) {
+#pragma unroll
+        for (uint32_t q = 0; q < 2; ++q) {
+            first[q] = slab * kSlab + q * 256 + lane * 4;
+            n[q] = first[q] < dim ? (uint32_t)min((uint64_t)4, dim - first[q]) : 0;
+        }
+    }
+};
+
+typedef u32x2 u32x2_any2 __attribute__((aligned(2)));
+
+// Loads without branches, so that those of several rows are in flight
+// together: columns outside are read at the row's end instead, for nothing.
+template <int DT, bool WHOLE>
+__device__ __forceinline__ void load_columns(const typename Plain<DT>::type *row, const Columns<WHOLE> &c,
+                                             float v[8]) {
+#pragma unroll
+    for (uint32_t q = 0; q < 2; ++q) {
+        float *x = v + 4 * q;
+        if constexpr (!WHOLE) {
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) x[i] = widen(row[min(c.first[q] + i, c.last)]);
+        } else if constexpr (DT == PC_F32) {
+            const u32x4 a = *reinterpret_cast<const u32x4_any4 *>(row + min(c.first[q], c.last - 3));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = as_f32(a[i]);
+        } else {
+            const u32x2 a = *reinterpret_cast<const u32x2_any2 *>(row + min(c.first[q], c.last - 3));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t u = a[i];
+                if constexpr (DT == PC_BF16) {
+                    x[2 * i] = as_f32(u << 16);
+                    x[2 * i + 1] = as_f32(u & 0xFFFF0000u);
+                } else {
+                    const f16x2 h = __builtin_bit_cast(f16x2, u);
+                    x[2 * i] = (float)h[0];
+                    x[2 * i + 1] = (float)h[1];
+                }
+            }
+        }
+    }
+}
+
+// Holds the rows loaded so far apart from their use, which the compiler would
+// otherwise bring together again, one row at a time.
+__device__ __forceinline__ void loaded(float v[kAhead][8]) {
+#pragma unroll
+    for (uint32_t k = 0; k < kAhead; ++k)
+        asm volatile("" : "+v"(v[k][0]), "+v"(v[k][1]), "+v"(v[k][2]), "+v"(v[k][3]), "+v"(v[k][4]), "+v"(v[k][5]),
+                     "+v"(v[k][6]), "+v"(v[k][7]));
+}
+
+template <int DT, bool STREAM, bool WHOLE>
+__device__ __forceinline__ void store_columns(typename Plain<DT>::type *row, const Columns<WHOLE> &c,
+                                              const float v[8]) {
+    typedef typename Plain<DT>::type T;
+    typedef T t4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (uint32_t q = 0; q < 2; ++q) {
+        T *p = row + c.first[q];
+        const float *x = v + 4 * q;
+        if (c.n[q] == 4) {
+            const f32x4 f = {x[0], x[1], x[2], x[3]};
+            put<sizeof(T), STREAM>(p, __builtin_convertvector(f, t4));
+        } else if (!WHOLE) {
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i)
+                if (i < c.n[q]) p[i] = (T)x[i];
+        }
+    }
+}
+
+struct Target {  // of a row's sum
+    float scale;
+    uint32_t add;
+};
+
+template <int ODT, bool WHOLE>
+__device__ __forceinline__ void put_row(typename Plain<ODT>::type *row, const Columns<WHOLE> &c, const float v[8],
+                                        const Target &to) {
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = v[i] * to.scale;
+    if (to.add) {
+        float old[8];
+        load_columns<ODT>(row, c, old);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] += old[i];
+    }
+    store_columns<ODT, true>(row, c, s);
+}
+
+// Few tokens: one launch.  A workgroup owns a range of the table's rows and a
+// slab of columns.  It reads all tokens, keeps those of its range in LDS (in
+// order, with their places), and its waves sum the rows one by one; a row
+// with many tokens is summed by all waves, a share of its tokens each.  Rows
+// without tokens become zero in passing.
+constexpr uint32_t kSmall = 1024;        // tokens
+constexpr uint32_t kSmallThreads = 256;
+constexpr uint32_t kSmallWaves = kSmallThreads / kWave;
+constexpr uint32_t kMany = 32;           // tokens of a row that are shared among the waves
+
+template <int DT, int ODT, typename TOK, bool WHOLE>
+__global__ __launch_bounds__(kSmallThreads) void small_kernel(const void *__restrict__ tokens, uint32_t n,
+                                                              const typename Plain<DT>::type *__restrict__ dy,
+                                                              uint64_t ld_dy, uint64_t vocab, uint64_t dim,
+                                                              int64_t padding, uint32_t range, Target to,
+                                                              typename Plain<ODT>::type *__restrict__ grad,
+                                                              uint64_t ld_grad) {
+    __shared__ uint32_t key[kSmall], place[kSmall];
+    __shared__ uint32_t sums[kSmallWaves];
+    __shared__ float part[kSmallWaves][kUnit][kWave];
+    const uint32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
+    const uint64_t lo = (uint64_t)blockIdx.x * range;
+    const uint32_t size = (uint32_t)min((uint64_t)range, vocab - lo);
+    // each wave a consecutive part of the tokens, up to 4 in a lane
+    constexpr uint32_t kEach = kSmall / kSmallThreads;
+    const uint32_t per = (n + kSmallThreads - 1) / kSmallThreads * kWave;
+    uint32_t mine[kEach];
+    uint64_t found[kEach];
+    uint32_t total = 0;
+#pragma unroll
+    for (uint32_t j = 0; j < kEach; ++j) {
+        const uint32_t at = j * kWave + lane, i = wave * per + at;
+        mine[j] = ~0u;
+        if (at < per && i < n) {
+            const int64_t t = token_at<TOK>(tokens, i);
+            if (t >= 0 && t != padding && (uint64_t)t >= lo && (uint64_t)t - lo < size) mine[j] = (uint32_t)(t - lo);
+        }
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < kEach; ++j) {
+        found[j] = __ballot(mine[j] != ~0u);
+        total += __popcll(found[j]);
+    }
+    if (lane == 0) sums[wave] = total;
+    __syncthreads();
+    uint32_t at = 0, count = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < kSmallWaves; ++w) {
+        if (w < wave) at += sums[w];
+        count += sums[w];
+    }
+    count = uniform(count);
+#pragma unroll
+    for (uint32_t j = 0; j < kEach; ++j) {
+        if (mine[j] != ~0u) {
+            const uint32_t p = at + __popcll(found[j] & ((1ull << lane) - 1));
+            key[p] = mine[j];
+            place[p] = wave * per + j * kWave + lane;
+        }
+        at += __popcll(found[j]);
+    }
+    __syncthreads();
+
+    const Columns<WHOLE> cols(blockIdx.y, lane, dim);
+    // sums row r over the list's groups of 64 entries first, first + step, ...
+    auto sum = [&](uint32_t r, uint32_t first, uint32_t step, float acc[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+        for (uint32_t g = first * kWave; g < count; g += step * kWave) {
+            const uint32_t e = g + lane;
+            const bool is = e < count && key[e] == r;
+            const uint32_t where = is ? place[e] : 0;
+            uint64_t left = __ballot(is);
+            while (left) {
+                float v[kAhead][8];
+                uint32_t from = 0;
+                auto next = [&](uint32_t k) {
+                    from = left ? (uint32_t)__builtin_ctzll(left) : from;
+                    left &= left - 1;
+                    const uint64_t t = (uint32_t)__builtin_amdgcn_readlane((int)where, (int)from);
+                    load_columns<DT>(dy + t * ld_dy, cols, v[k]);
+                };
+                const uint32_t got = min(kAhead, (uint32_t)__popcll(left));
+                if (got == 1) {
+                    next(0);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[i] += v[0][i];
+                    continue;
+                }
+#pragma unroll
+                for (uint32_t k = 0; k < kAhead; ++k) next(k);  // past the last one the last again
+                loaded(v);
+#pragma unroll
+                for (uint32_t k = 0; k < kAhead; ++k)
+                    if (k < got)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) acc[i] += v[k][i];
+            }
+        }
+    };
+    auto tokens_of = [&](uint32_t r) {
+        uint32_t c = 0;
+        for (uint32_t g = 0; g < count; g += kWave) c += __popcll(__ballot(g + lane < count && key[g + lane] == r));
+        return c;
+    };
+    // Row by row; or, where nothing is written to rows without tokens and the
+    // range has more rows than tokens, token by token, a row at its first.
+    const bool by_token = to.add && count < size;
+    const uint32_t many = by_token ? count : size;
+    auto row_at = [&](uint32_t q) -> uint32_t {
+        if (!by_token) return q;
+        const uint32_t r = uniform(key[q]);
+        for (uint32_t g = 0; g < q; g += kWave)
+            if (__ballot(g + lane < q && key[g + lane] == r)) return ~0u;
+        return r;
+    };
+    float acc[8];
+    for (uint32_t q = wave; q < many; q += kSmallWaves) {
+        const uint32_t r = row_at(q);
+        if (r == ~0u) continue;
+        const uint32_t c = tokens_of(r);
+        if (c > kMany || (c == 0 && to.add)) continue;
+        sum(r, 0, 1, acc);
+        put_row<ODT>(grad + (lo + r) * ld_grad, cols, acc, to);
+    }
+    if (count <= kMany) return;
+    for (uint32_t q = 0; q < many; ++q) {
+        const uint32_t r = row_at(q);
+        if (r == ~0u || tokens_of(r) <= kMany) continue;
+        sum(r, wave, kSmallWaves, acc);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) part[wave][i][lane] = acc[i];
+        __syncthreads();
+        if (wave == 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                for (uint32_t w = 1; w < kSmallWaves; ++w) acc[i] += part[w][i][lane];
+            put_row<ODT>(grad + (lo + r) * ld_grad, cols, acc, to);
+        }
+        __syncthreads();
+    }
+}
+
+// More tokens: sort, sum, join.  Workspace: start[vocab + 1] (first sorted
+// place of each token), key[n] and source[n] (token and row of dy at each
+// sorted place), partial sums of the runs that cross a block's end.
 struct Sorted {
     uint32_t *start, *key, *source;
     float *part;  // [blocks][2][dim]: a block's sum for a run from an earlier block, and for one that goes on
@@ -84,6 +330,9 @@ struct Sorted {
 constexpr uint32_t kSortThreads = 1024;
 constexpr uint32_t kSortWaves = kSortThreads / kWave;
 constexpr uint32_t kMaxRange = 1000;  // tokens (rows of the table) of one workgroup: 16 counters each, in 64 KB of LDS
+constexpr uint32_t kTokensAhead = 8;
+constexpr uint32_t kKept = 4;  // groups of 8 tokens that stay in a lane's registers
+constexpr uint32_t kResident = kSortThreads * kTokensAhead * kKept;
 
 // One workgroup sorts the tokens of one range of the vocabulary.  It reads
 // all tokens (they stay in the L2), each wave a part of them in order: once
@@ -91,11 +340,12 @@ constexpr uint32_t kMaxRange = 1000;  // tokens (rows of the table) of one workg
 // starts, and each token of its range by wave; then again to place them.
 // Tokens of one value keep their order: waves hold consecutive parts, and in
 // a wave the lanes with the same token find each other by one vote per bit.
-template <typename TOK>
+// Up to 32768 tokens stay in registers between the two.
+template <typename TOK, bool RESIDENT>
 __global__ __launch_bounds__(kSortThreads) void sort_kernel(const void *__restrict__ tokens, uint32_t n,
                                                             uint64_t vocab, int64_t padding, uint32_t range,
                                                             uint32_t bits, Sorted out) {
-    extern __shared__ uint32_t cnt[];  // [kSortWaves][range], then kSortWaves + 1 words
+    extern __shared__ uint32_t cnt[];  // [kSortWaves][range], then kSortWaves words
     uint32_t *sums = cnt + kSortWaves * range;
     const uint32_t tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
     const uint64_t lo = (uint64_t)blockIdx.x * range;
@@ -105,12 +355,40 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const void *__restri
     uint32_t *my = cnt + wave * range;
     const uint32_t part = (n + kSortWaves * kWave - 1) / (kSortWaves * kWave) * kWave;
     const uint32_t first = min(n, wave * part), last = min(n, first + part);
+    // tokens i0 + lane, i0 + 64 + lane, ..: their number in the range, -1 for
+    // one below it, -2 for any other
+    auto fetch = [&](uint32_t i0, int32_t r[kTokensAhead]) {
+        int64_t t[kTokensAhead];
+#pragma unroll
+        for (uint32_t k = 0; k < kTokensAhead; ++k) {
+            const uint32_t i = i0 + k * kWave + lane;
+            t[k] = i < last ? token_at<TOK>(tokens, i) : -1;
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < kTokensAhead; ++k) {
+            const bool ok = t[k] >= 0 && (uint64_t)t[k] < vocab && t[k] != padding;
+            r[k] = !ok ? -2 : (uint64_t)t[k] < lo ? -1 : (uint64_t)t[k] - lo < size ? (int32_t)(t[k] - lo) : -2;
+        }
+    };
     uint32_t below = 0;
-    for (uint32_t i = first + lane; i < last; i += kWave) {
-        const int64_t t = token_at<TOK>(tokens, i);
-        if (t < 0 || (uint64_t)t >= vocab || t == padding) continue;
-        if ((uint64_t)t < lo) ++below;
-        else if ((uint64_t)t - lo < size) atomicAdd(&my[(uint64_t)t - lo], 1u);
+    int32_t kept[kKept][kTokensAhead];
+    auto count = [&](const int32_t r[kTokensAhead]) {
+#pragma unroll
+        for (uint32_t k = 0; k < kTokensAhead; ++k) {
+            below += r[k] == -1;
+            if (r[k] >= 0) atomicAdd(&my[r[k]], 1u);
+        }
+    };
+    if constexpr (RESIDENT) {
+#pragma unroll
+        for (uint32_t g = 0; g < kKept; ++g) fetch(first + g * kTokensAhead * kWave, kept[g]);
+#pragma unroll
+        for (uint32_t g = 0; g < kKept; ++g) count(kept[g]);
+    } else {
+        for (uint32_t i0 = first; i0 < last; i0 += kTokensAhead * kWave) {
+            fetch(i0, kept[0]);
+            count(kept[0]);
+        }
     }
 #pragma unroll
     for (int m = 32; m >= 1; m >>= 1) below += __shfl_xor(below, m, 64);
@@ -120,22 +398,20 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const void *__restri
     for (uint32_t w = 0; w < kSortWaves; ++w) base += sums[w];
     __syncthreads();
     // start of every token of the range, and of every wave's share of it
-    for (uint32_t r0 = 0; r0 < size; r0 += kSortThreads) {
-        const uint32_t r = r0 + tid;
+    {
+        const uint32_t r = tid;
         uint32_t total = 0;
         if (r < size)
             for (uint32_t w = 0; w < kSortWaves; ++w) total += cnt[w * range + r];
         const uint32_t incl = wave_incl_scan(total);
         if (lane == kWave - 1) sums[wave] = incl;
         __syncthreads();
-        uint32_t before = 0, all = 0;
+        uint32_t at = base + incl - total;
         for (uint32_t w = 0; w < kSortWaves; ++w) {
-            if (w < wave) before += sums[w];
-            all += sums[w];
+            if (w < wave) at += sums[w];
+            base += sums[w];
         }
-        __syncthreads();
         if (r < size) {
-            uint32_t at = base + before + incl - total;
             out.start[lo + r] = at;
             for (uint32_t w = 0; w < kSortWaves; ++w) {
                 const uint32_t c = cnt[w * range + r];
@@ -143,142 +419,152 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const void *__restri
                 at += c;
             }
         }
-        base += all;
     }
     if (tid == 0 && lo + size == vocab) out.start[vocab] = base;
     __syncthreads();
-    for (uint32_t i0 = first; i0 < last; i0 += kWave) {
-        const uint32_t i = i0 + lane;
-        const int64_t t = i < last ? token_at<TOK>(tokens, i) : -1;
-        const bool mine = t >= 0 && t != padding && (uint64_t)t >= lo && (uint64_t)t - lo < size;
-        uint64_t same = __ballot(mine);
-        if (!same) continue;
-        const uint32_t r = mine ? (uint32_t)((uint64_t)t - lo) : 0;
-        for (uint32_t b = 0; b < bits; ++b) {
-            const uint64_t set = __ballot(r >> b & 1);
-            same &= (r >> b & 1) ? set : ~set;
+    auto place = [&](const int32_t r[kTokensAhead], uint32_t i0) {
+#pragma unroll
+        for (uint32_t k = 0; k < kTokensAhead; ++k) {
+            const bool mine = r[k] >= 0;
+            uint64_t same = __ballot(mine);
+            if (!same) continue;
+            for (uint32_t b = 0; b < bits; ++b) {
+                const uint64_t set = __ballot(r[k] >> b & 1);
+                same &= (r[k] >> b & 1) ? set : ~set;
+            }
+            const uint32_t before = __popcll(same & ((1ull << lane) - 1));
+            if (mine) {
+                const uint32_t at = my[r[k]] + before;
+                out.key[at] = (uint32_t)(lo + r[k]);
+                out.source[at] = i0 + k * kWave + lane;
+            }
+            __builtin_amdgcn_wave_barrier();
+            if (mine && before == 0) atomicAdd(&my[r[k]], (uint32_t)__popcll(same));
+            __builtin_amdgcn_wave_barrier();
         }
-        const uint32_t before = __popcll(same & ((1ull << lane) - 1));
-        if (mine) {
-            const uint32_t at = my[r] + before;
-            out.key[at] = (uint32_t)t;
-            out.source[at] = i;
+    };
+    if constexpr (RESIDENT) {
+#pragma unroll
+        for (uint32_t g = 0; g < kKept; ++g) place(kept[g], first + g * kTokensAhead * kWave);
+    } else {
+        for (uint32_t i0 = first; i0 < last; i0 += kTokensAhead * kWave) {
+            fetch(i0, kept[0]);
+            place(kept[0], i0);
         }
-        __builtin_amdgcn_wave_barrier();
-        if (mine && before == 0) atomicAdd(&my[r], (uint32_t)__popcll(same));
-        __builtin_amdgcn_wave_barrier();
     }
 }
-
-template <int ODT>
-__device__ __forceinline__ void put_row(typename Plain<ODT>::type *p, uint32_t n, const float v[8], float scale,
-                                        bool add) {
-    float s[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = v[i] * scale;
-    if (add) {
-        float old[8];
-        load_unit<ODT>(p, n, old);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] += old[i];
-    }
-    store_unit<ODT>(p, n, s);
-}
-
-constexpr uint32_t kSlab = kWave * kUnit;  // columns of one wave
 
 // A wave sums one block of sorted places over one slab of columns: whole runs
 // go to the gradient, a run that crosses a block's end leaves partial sums.
 // Waves past those write the zeros of the rows that no token names.
-template <int DT, int ODT>
+template <int DT, int ODT, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void sum_kernel(const typename Plain<DT>::type *__restrict__ dy,
                                                        uint64_t ld_dy, Sorted in, uint64_t vocab, uint64_t dim,
-                                                       uint32_t block, uint32_t blocks, uint32_t slabs, float scale,
+                                                       uint32_t block, uint32_t blocks, uint32_t slabs, Target to,
                                                        typename Plain<ODT>::type *__restrict__ grad,
-                                                       uint64_t ld_grad, uint32_t add) {
+                                                       uint64_t ld_grad) {
     const uint32_t lane = threadIdx.x % kWave;
     const uint64_t id = (uint64_t)blockIdx.x * (kThreads / kWave) + uniform(threadIdx.x / kWave);
     const uint64_t work = (uint64_t)blocks * slabs;
     if (id >= work) {
-        if (add) return;
-        const uint64_t v = id - work;
-        if (v >= vocab || in.start[v] != in.start[v + 1]) return;
+        const uint64_t v = id - work;  // (none where rows are added to: the grid's last waves)
+        if (to.add || v >= vocab || in.start[v] != in.start[v + 1]) return;
         const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (uint64_t c = lane * kUnit; c < dim; c += kSlab)
-            store_unit<ODT>(grad + v * ld_grad + c, (uint32_t)min((uint64_t)kUnit, dim - c), zero);
+        for (uint32_t slab = 0; slab < slabs; ++slab)
+            store_columns<ODT, true>(grad + v * ld_grad, Columns<WHOLE>(slab, lane, dim), zero);
         return;
     }
     const uint32_t b = (uint32_t)(id / slabs);
-    const uint64_t col = (id % slabs) * kSlab + lane * kUnit;
-    const uint32_t n = col < dim ? (uint32_t)min((uint64_t)kUnit, dim - col) : 0;
-    const uint32_t count = in.start[vocab];
+    const Columns<WHOLE> cols(id % slabs, lane, dim);
+    const uint32_t count = uniform(in.start[vocab]);
     const uint32_t p0 = b * block;
     if (p0 >= count) return;
-    const uint32_t p1 = min(count, p0 + block);
-    uint32_t p = p0;
-    while (p < p1) {
-        const uint32_t key = uniform(in.key[p]);
-        const uint32_t begin = uniform(in.start[key]), end = uniform(in.start[key + 1]);
-        const uint32_t stop = min(p1, end);
-        float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (; p < stop; ++p) {
-            const uint64_t t = uniform(in.source[p]);
-            if (n) {
-                float v[8];
-                load_unit<DT>(dy + t * ld_dy + col, n, v);
+    const uint32_t places = min(block, count - p0);  // at most 32
+    // lane i: the key of place p0 + i - 1 (lane 0 the place before the block, if any), the row of place p0 + i
+    const bool has = lane <= places + 1 && p0 + lane >= 1 && p0 + lane - 1 < count;
+    const uint32_t key = has ? in.key[p0 + lane - 1] : ~0u;
+    const uint32_t source = lane < places ? in.source[p0 + lane] : 0;
+    const uint32_t next = (uint32_t)__shfl_down((int)key, 1, 64);
+    const uint64_t change = __ballot(key != next);  // bit i: places p0 + i - 1 and p0 + i differ
+    const bool from_before = !(change & 1);
+    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    bool first = true;
+    for (uint32_t i0 = 0; i0 < places; i0 += kAhead) {
+        float v[kAhead][8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] += v[i];
-            }
+        for (uint32_t k = 0; k < kAhead; ++k) {
+            const uint32_t i = min(i0 + k, places - 1);
+            const uint64_t t = (uint32_t)__builtin_amdgcn_readlane((int)source, (int)i);
+            load_columns<DT>(dy + t * ld_dy, cols, v[k]);
         }
-        if (!n) continue;
-        if (begin >= p0 && end <= p0 + block)
-            put_row<ODT>(grad + (uint64_t)key * ld_grad + col, n, acc, scale, add);
-        else
-            store_unit<PC_F32>(in.part + ((uint64_t)b * 2 + (begin >= p0)) * dim + col, n, acc);
+        loaded(v);
+#pragma unroll
+        for (uint32_t k = 0; k < kAhead; ++k) {
+            const uint32_t i = i0 + k;
+            if (i >= places) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] += v[k][j];
+            const bool end = change >> (i + 1) & 1;
+            if (!end && i + 1 < places) continue;
+            const bool before = first && from_before;
+            if (end && !before) {
+                const uint64_t row = (uint32_t)__builtin_amdgcn_readlane((int)key, (int)i + 1);
+                put_row<ODT>(grad + row * ld_grad, cols, acc, to);
+            } else {
+                store_columns<PC_F32, false>(in.part + ((uint64_t)b * 2 + !before) * dim, cols, acc);
+            }
+            first = false;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+        }
     }
 }
 
 // Joins the partial sums of the run that starts in block b and crosses its
 // end, in the order of the blocks: each wave of the workgroup takes an equal
 // share of them, and wave 0 adds up the waves.
-template <int ODT>
+template <int ODT, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void join_kernel(Sorted in, uint64_t vocab, uint64_t dim, uint32_t block,
-                                                        uint32_t slabs, float scale,
+                                                        uint32_t slabs, Target to,
                                                         typename Plain<ODT>::type *__restrict__ grad,
-                                                        uint64_t ld_grad, uint32_t add) {
+                                                        uint64_t ld_grad) {
     __shared__ float part[kThreads / kWave][kUnit][kWave];
-    const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const uint32_t b = blockIdx.x / slabs;
-    const uint64_t col = (uint64_t)(blockIdx.x % slabs) * kSlab + lane * kUnit;
-    const uint32_t n = col < dim ? (uint32_t)min((uint64_t)kUnit, dim - col) : 0;
-    const uint32_t count = in.start[vocab];
-    const uint32_t p1 = (b + 1) * block;
-    if (p1 >= count) return;
-    const uint32_t key = in.key[p1 - 1];
-    const uint32_t begin = in.start[key], end = in.start[key + 1];
-    if (end <= p1 || begin < b * block) return;
+    const uint32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
+    const uint32_t b = blockIdx.x / slabs, p1 = (b + 1) * block;  // below the number of tokens
+    const Columns<WHOLE> cols(blockIdx.x % slabs, lane, dim);
+    const uint32_t count = uniform(in.start[vocab]), key = uniform(in.key[p1 - 1]), next = uniform(in.key[p1]);
+    if (p1 >= count || key != next) return;
+    const uint32_t begin = uniform(in.start[key]), end = uniform(in.start[key + 1]);
+    if (begin < b * block) return;
     const uint32_t last = (end - 1) / block;  // the run's parts: block b's second, then the first of b + 1 .. last
     const uint32_t each = (last - b + 1 + kThreads / kWave - 1) / (kThreads / kWave);
-    const uint32_t from = b + wave * each, to = min(last + 1, from + each);
+    const uint32_t from = b + wave * each, till = min(last + 1, from + each);
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (n)
-        for (uint32_t i = from; i < to; ++i) {
-            float v[8];
-            load_unit<PC_F32>(in.part + ((uint64_t)i * 2 + (i == b)) * dim + col, n, v);
+    for (uint32_t i0 = from; i0 < till; i0 += kAhead) {
+        float v[kAhead][8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) acc[k] += v[k];
+        for (uint32_t k = 0; k < kAhead; ++k) {
+            const uint64_t i = min(i0 + k, till - 1);
+            load_columns<PC_F32>(in.part + (i * 2 + (i == b)) * dim, cols, v[k]);
         }
+        loaded(v);
+#pragma unroll
+        for (uint32_t k = 0; k < kAhead; ++k)
+            if (i0 + k < till)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[j] += v[k][j];
+    }
 #pragma unroll
     for (int k = 0; k < 8; ++k) part[wave][k][lane] = acc[k];
     __syncthreads();
-    if (wave || !n) return;
+    if (wave) return;
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         for (uint32_t w = 1; w < kThreads / kWave; ++w) acc[k] += part[w][k][lane];
-    put_row<ODT>(grad + (uint64_t)key * ld_grad + col, n, acc, scale, add);
+    put_row<ODT>(grad + (uint64_t)key * ld_grad, cols, acc, to);
 }
 
-constexpr uint32_t kBlock = 32;  // sorted places summed by one wave
+constexpr uint32_t kBlock = 32;  // sorted places summed by one wave (two lanes are left for its neighbours)
 
 uint32_t range_of(uint64_t vocab) {
     const uint64_t r = std::max<uint64_t>(64, (vocab + 255) / 256);
@@ -290,6 +576,7 @@ uint64_t up16(uint64_t b) { return (b + 15) / 16 * 16; }
 }  // namespace
 
 uint64_t embed_backward_workspace(uint64_t n, uint64_t dim, uint64_t vocab) {
+    if (n <= kSmall) return 0;
     const uint64_t blocks = (n + kBlock - 1) / kBlock;
     return up16((vocab + 1) * 4) + 2 * up16(n * 4) + up16(blocks * 2 * dim * 4);
 }
@@ -323,8 +610,34 @@ hipError_t launch_embed(const void *tokens, int token_bytes, uint64_t n, const v
 hipError_t launch_embed_backward(const void *dy, int dtype, uint64_t ld_dy, const void *tokens, int token_bytes,
                                  uint32_t n, uint64_t dim, uint64_t vocab, int64_t padding, float scale, void *grad,
                                  int grad_dtype, uint64_t ld_grad, bool accumulate, void *ws, hipStream_t stream) {
-    const uint32_t range = range_of(vocab), blocks = (n + kBlock - 1) / kBlock;
     const uint32_t slabs = (uint32_t)((dim + kSlab - 1) / kSlab);
+    const Target to = {scale, accumulate};
+    const bool whole = dim % 4 == 0;
+    if (n <= kSmall) {
+        // about 2048 workgroups, of at least 4 rows: each reads all tokens
+        const uint64_t each = std::min<uint64_t>(1u << 20, std::max<uint64_t>(4, vocab * slabs / 2048));
+        const dim3 grid((uint32_t)((vocab + each - 1) / each), slabs);
+        with_dtype(grad_dtype, [&](auto o) {
+            constexpr int ODT = decltype(o)::value;
+            with_dtype(dtype, [&](auto d) {
+                constexpr int DT = decltype(d)::value;
+                auto launch = [&](auto k) {
+                    hipLaunchKernelGGL(k, grid, dim3(kSmallThreads), 0, stream, tokens, n,
+                                       static_cast<const typename Plain<DT>::type *>(dy), ld_dy, vocab, dim, padding,
+                                       (uint32_t)each, to, static_cast<typename Plain<ODT>::type *>(grad), ld_grad);
+                };
+                auto by_width = [&](auto w) {
+                    constexpr bool WHOLE = decltype(w)::value;
+                    token_bytes == 8 ? launch(small_kernel<DT, ODT, int64_t, WHOLE>)
+                                     : launch(small_kernel<DT, ODT, int32_t, WHOLE>);
+                };
+                if (whole) by_width(std::true_type());
+                else by_width(std::false_type());
+            });
+        });
+        return hipGetLastError();
+    }
+    const uint32_t range = range_of(vocab), blocks = (n + kBlock - 1) / kBlock;
     uint32_t bits = 0;
     while ((1u << bits) < range) ++bits;
     uint8_t *p = static_cast<uint8_t *>(ws);
@@ -337,26 +650,30 @@ hipError_t launch_embed_backward(const void *dy, int dtype, uint64_t ld_dy, cons
     p += up16((uint64_t)n * 4);
     s.part = reinterpret_cast<float *>(p);
     const dim3 ranges((uint32_t)((vocab + range - 1) / range));
-    const uint32_t lds = (kSortWaves * range + kSortWaves + 1) * 4;
+    const uint32_t lds = (kSortWaves * range + kSortWaves) * 4;
     auto sort = [&](auto k) {
         hipLaunchKernelGGL(k, ranges, dim3(kSortThreads), lds, stream, tokens, n, vocab, padding, range, bits, s);
     };
-    token_bytes == 8 ? sort(sort_kernel<int64_t>) : sort(sort_kernel<int32_t>);
+    if (n <= kResident) token_bytes == 8 ? sort(sort_kernel<int64_t, true>) : sort(sort_kernel<int32_t, true>);
+    else token_bytes == 8 ? sort(sort_kernel<int64_t, false>) : sort(sort_kernel<int32_t, false>);
     const uint64_t waves = (uint64_t)blocks * slabs + (accumulate ? 0 : vocab);
     const dim3 grid((uint32_t)((waves + kThreads / kWave - 1) / (kThreads / kWave)));
-    with_dtype(grad_dtype, [&](auto o) {
+    auto sums = [&](auto o, auto w) {
         constexpr int ODT = decltype(o)::value;
+        constexpr bool WHOLE = decltype(w)::value;
         typedef typename Plain<ODT>::type T;
-        if (grid.x)
-            with_dtype(dtype, [&](auto d) {
-                constexpr int DT = decltype(d)::value;
-                hipLaunchKernelGGL((sum_kernel<DT, ODT>), grid, dim3(kThreads), 0, stream,
-                                   static_cast<const typename Plain<DT>::type *>(dy), ld_dy, s, vocab, dim, kBlock,
-                                   blocks, slabs, scale, static_cast<T *>(grad), ld_grad, (uint32_t)accumulate);
-            });
-        if (blocks > 1)
-            hipLaunchKernelGGL(join_kernel<ODT>, dim3((blocks - 1) * slabs), dim3(kThreads), 0, stream, s, vocab, dim,
-                               kBlock, slabs, scale, static_cast<T *>(grad), ld_grad, (uint32_t)accumulate);
+        with_dtype(dtype, [&](auto d) {
+            constexpr int DT = decltype(d)::value;
+            hipLaunchKernelGGL((sum_kernel<DT, ODT, WHOLE>), grid, dim3(kThreads), 0, stream,
+                               static_cast<const typename Plain<DT>::type *>(dy), ld_dy, s, vocab, dim, kBlock, blocks,
+                               slabs, to, static_cast<T *>(grad), ld_grad);
+        });
+        hipLaunchKernelGGL((join_kernel<ODT, WHOLE>), dim3((blocks - 1) * slabs), dim3(kThreads), 0, stream, s, vocab,
+                           dim, kBlock, slabs, to, static_cast<T *>(grad), ld_grad);
+    };
+    with_dtype(grad_dtype, [&](auto o) {
+        if (whole) sums(o, std::true_type());
+        else sums(o, std::false_type());
     });
     return hipGetLastError();
 }

@@ -22,12 +22,14 @@ constexpr uint32_t kTile = kThreads * kPerLane;
 // store
 // ---------------------------------------------------------------------------
 
-// Histogram of the symbols in LDS, as in the byte histogram: 16 copies per
-// wave, 257 words apart, added to the caller's counts at the end.
-constexpr uint32_t kCopies = 16;
+// Histogram of the symbols in LDS, as in the byte histogram but with 8 copies
+// per wave, 257 words apart, added to the caller's counts at the end.  33 KB
+// a workgroup, so that four fit a CU: with 16 copies and two workgroups the
+// loads of 64 Mi bf16 elements waited (89 us; 67 us with 8).
+constexpr uint32_t kCopies = 8;
 constexpr uint32_t kCopyStride = 257;
 constexpr uint32_t kBins = kThreads / kWave * kCopies * kCopyStride;
-constexpr uint32_t kCountBlocks = 512;  // 66 KB of LDS each: two per CU
+constexpr uint32_t kCountBlocks = 1024;
 
 __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
     v = max(v, dpp_u32<0xB1>(v));  // neighbour in the pair

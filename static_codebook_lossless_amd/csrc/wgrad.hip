@@ -48,8 +48,9 @@ __device__ __forceinline__ uint32_t term_bits(float v, uint32_t which) {
 // past `bytes` reads 0.
 typedef __amdgpu_buffer_rsrc_t Buffer;
 __device__ __forceinline__ Buffer make_buffer(const void *p, uint64_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)(uint32_t)min(bytes, (uint64_t)0xFFFFFFFFu),
-                                             0x00020000);
+    const uint64_t at = uniform64(reinterpret_cast<uint64_t>(p));
+    const uint32_t most = uniform((uint32_t)min(bytes, (uint64_t)0xFFFFFFFFu));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(at), 0, (int)most, 0x00020000);
 }
 
 // A block of 8 rows of 8 columns as loaded: rows of 8 elements of dy, or of
@@ -58,11 +59,12 @@ template <int DT> struct RawDy {
     static constexpr uint32_t kWords = DT == PC_F32 ? 2 : 1;
     u32x4 w[8][kWords];
 
-    __device__ __forceinline__ void load(Buffer b, const uint32_t at[8]) {
+    __device__ __forceinline__ void load(Buffer b, uint32_t at, uint32_t row) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
-            for (uint32_t k = 0; k < kWords; ++k) w[i][k] = __builtin_amdgcn_raw_buffer_load_b128(b, at[i] + 16 * k, 0, 0);
+            for (uint32_t k = 0; k < kWords; ++k)
+                w[i][k] = __builtin_amdgcn_raw_buffer_load_b128(b, at + i * row + 16 * k, 0, 0);
     }
     // the first n elements of row i, each by itself
     __device__ __forceinline__ void load_single(int i, Buffer b, uint32_t at, uint32_t n) {
@@ -103,11 +105,12 @@ template <int FMT> struct RawX {
     u32x2 w[8];
     uint32_t code[8];
 
-    __device__ __forceinline__ void load(Buffer b, const uint32_t at[8], Buffer codes, const uint32_t code_at[8]) {
+    __device__ __forceinline__ void load(Buffer b, uint32_t at, uint32_t row, Buffer codes, uint32_t code_at,
+                                         uint32_t code_row) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            w[i] = __builtin_amdgcn_raw_buffer_load_b64(b, at[i], 0, 0);
-            code[i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(codes, code_at[i], 0, 0);
+            w[i] = __builtin_amdgcn_raw_buffer_load_b64(b, at + i * row, 0, 0);
+            code[i] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(codes, code_at + i * code_row, 0, 0);
         }
     }
     __device__ __forceinline__ void load_single(int i, Buffer b, uint32_t at, uint32_t n) {
@@ -177,12 +180,40 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-template <int DT, int FMT, int ODT, uint32_t WN, uint32_t WK, uint32_t FN, uint32_t FK>
+// The order of a step's instructions up to its barrier: between two matrix
+// instructions (of a step's three quarters of M each) a share of everything
+// else, so that the matrix cores never wait for a run of other work.
+template <uint32_t M>
+__device__ __forceinline__ void interleave() {
+    if constexpr (M == 16) {
+#pragma unroll
+        for (uint32_t m = 0; m < 3 * M; ++m) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                    // matrix
+            if (m % M < 8) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                     // LDS read
+            __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);                                    // vector
+            if (m >= 4 && m % 2 == 1 && m < 40) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);  // LDS write
+            if (m >= 20 && m < 28) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);             // load
+            if (m >= 40) __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);
+        }
+    }
+}
+template <uint32_t M, uint32_t R>
+__device__ __forceinline__ void interleave_tail() {
+    if constexpr (M == 16) {
+#pragma unroll
+        for (uint32_t m = 0; m < R; ++m) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, M - R, 0);
+    }
+}
+
+template <int DT, int FMT, bool RAGGED, uint32_t WN, uint32_t WK, uint32_t FN, uint32_t FK>
 __global__ __launch_bounds__(WN *WK *kWave, 1) void wgrad_kernel(const typename Plain<DT>::type *__restrict__ dy,
                                                                  const uint8_t *__restrict__ sym,
                                                                  const uint8_t *__restrict__ scale, Shape s,
-                                                                 typename Plain<ODT>::type *__restrict__ out,
-                                                                 uint32_t add) {
+                                                                 void *__restrict__ out, int out_dtype, uint32_t add) {
     constexpr uint32_t BN = WN * FN * 32, BK = WK * FK * 32, NT = WN * WK * kWave;
     constexpr uint32_t kElem = sizeof(typename Plain<DT>::type);
     // blocks of the two tiles: one of each for every lane, or one for every lane of either half
@@ -196,60 +227,68 @@ __global__ __launch_bounds__(WN *WK *kWave, 1) void wgrad_kernel(const typename 
     const uint32_t all = (uint32_t)((s.t + kStep - 1) / kStep);
     const uint32_t first = min(all, blockIdx.y * s.slice), tiles = min(all - first, s.slice);
     const uint32_t steps = tiles * kTerms<DT>;
-    if constexpr (ODT == PC_F32) out += (uint64_t)blockIdx.y * s.n * s.k;  // a slice's partial sums (one slice: the output)
 
     const bool has_dy = kBoth || wave < WN * WK / 2, has_x = kBoth || !has_dy;
     const uint32_t b = kBoth ? tid : tid % (NT / 2);
     const uint32_t yl = b % (BN / 8), yt = b / (BN / 8), xl = b % (BK / 8), xt = b / (BK / 8);
-    uint32_t y_at[8], x_at[8], c_at[8];
-#pragma unroll
-    for (uint32_t i = 0; i < 8; ++i) {
-        y_at[i] = (yt * 8 + i) * (uint32_t)s.ld_dy * kElem + yl * 8 * kElem;
-        x_at[i] = (xt * 8 + i) * (uint32_t)s.ld_sym + xl * 8;
-        c_at[i] = (xt * 8 + i) * (uint32_t)s.ld_scale + xl / kUnitsPerGroup;
-    }
+    const uint32_t y_row = (uint32_t)s.ld_dy * kElem, x_row = (uint32_t)s.ld_sym, c_row = (uint32_t)s.ld_scale;
+    const uint32_t y_at = yt * 8 * y_row + yl * 8 * kElem, x_at = xt * 8 * x_row + xl * 8;
+    const uint32_t c_at = xt * 8 * c_row + xl / kUnitsPerGroup;
     RawDy<DT> ry;
     RawX<FMT> rx;
 
+    // Rows from tile i's first to the tensor's last; none past the last tile.
+    auto rows_of = [&](uint32_t i, uint64_t &t0) -> uint64_t {
+        t0 = (uint64_t)(first + (kTerms<DT> == 1 ? i : i % tiles)) * kStep;
+        return i < steps ? s.t - t0 : 0;
+    };
     // Loads tile i (past the last: zeros) into registers.
-    auto load = [&](uint32_t i) {
-        const uint64_t t0 = (uint64_t)(first + (kTerms<DT> == 1 ? i : i % tiles)) * kStep;
-        const uint64_t rows = i < steps ? s.t - t0 : 0;  // rows from t0 to the tensor's end
-        const bool near = rows && rows < kStep + 8;
-        if (has_dy) {
-            const uint64_t bytes = rows ? ((rows - 1) * s.ld_dy + (s.n - n0)) * kElem : 0;
-            const Buffer buf = make_buffer(dy + (rows ? t0 * s.ld_dy + n0 : 0), bytes);
-            ry.load(buf, y_at);
-            // a block that sticks out of the tensor's last row: the load may have
-            // dropped the elements that are in it
-            const uint64_t c = n0 + yl * 8;
-            if (near && n0 + BN > s.n && c < s.n && c + 8 > s.n) {
+    auto load_dy = [&](uint32_t i) {
+        uint64_t t0;
+        const uint64_t rows = rows_of(i, t0), bytes = rows * y_row - (s.ld_dy - (s.n - n0)) * kElem;
+        if (has_dy) ry.load(make_buffer(dy + t0 * s.ld_dy + n0, rows ? bytes : 0), y_at, y_row);
+    };
+    auto load_x = [&](uint32_t i) {
+        uint64_t t0;
+        const uint64_t rows = rows_of(i, t0), bytes = rows * x_row - (s.ld_sym - (s.k - k0));
+        const uint64_t code_bytes = rows * c_row - (s.ld_scale - ((s.k + kGroup - 1) / kGroup - k0 / kGroup));
+        if (has_x)
+            rx.load(make_buffer(sym + t0 * s.ld_sym + k0, rows ? bytes : 0), x_at, x_row,
+                    make_buffer(scale + t0 * s.ld_scale + k0 / kGroup, rows ? code_bytes : 0), c_at, c_row);
+    };
+    // A block that sticks out of the tensor's last row (widths that are no
+    // multiple of 8): its load may have dropped elements that are inside.
+    // Only the last tiles of t meet one.
+    auto mend = [&](uint32_t i) {
+        if constexpr (!RAGGED) return;
+        uint64_t t0;
+        const uint64_t rows = rows_of(i, t0);
+        if (rows == 0 || rows >= kStep + 8) return;
+        const uint64_t cy = n0 + yl * 8, cx = k0 + xl * 8;
+        if (has_dy && cy < s.n && cy + 8 > s.n) {
+            const uint64_t bytes = ((rows - 1) * s.ld_dy + (s.n - n0)) * kElem;
+            const Buffer buf = make_buffer(dy + t0 * s.ld_dy + n0, bytes);
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (y_at[r] < bytes && y_at[r] + 8 * kElem > bytes)
-                        ry.load_single(r, buf, y_at[r], (uint32_t)(s.n - c));
+            for (int r = 0; r < 8; ++r) {
+                const uint32_t at = y_at + r * y_row;
+                if (at < bytes && at + 8 * kElem > bytes) ry.load_single(r, buf, at, (uint32_t)(s.n - cy));
             }
         }
-        if (has_x) {
-            const uint64_t bytes = rows ? (rows - 1) * s.ld_sym + (s.k - k0) : 0;
-            const Buffer buf = make_buffer(sym + (rows ? t0 * s.ld_sym + k0 : 0), bytes);
-            const uint64_t groups = (s.k + kGroup - 1) / kGroup - k0 / kGroup;
-            const Buffer codes = make_buffer(scale + (rows ? t0 * s.ld_scale + k0 / kGroup : 0),
-                                             rows ? (rows - 1) * s.ld_scale + groups : 0);
-            rx.load(buf, x_at, codes, c_at);
-            const uint64_t c = k0 + xl * 8;
-            if (near && k0 + BK > s.k && c < s.k && c + 8 > s.k) {
+        if (has_x && cx < s.k && cx + 8 > s.k) {
+            const uint64_t bytes = (rows - 1) * s.ld_sym + (s.k - k0);
+            const Buffer buf = make_buffer(sym + t0 * s.ld_sym + k0, bytes);
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (x_at[r] < bytes && x_at[r] + 8 > bytes) rx.load_single(r, buf, x_at[r], (uint32_t)(s.k - c));
+            for (int r = 0; r < 8; ++r) {
+                const uint32_t at = x_at + r * x_row;
+                if (at < bytes && at + 8 > bytes) rx.load_single(r, buf, at, (uint32_t)(s.k - cx));
             }
         }
     };
-    auto put_dy = [&](uint32_t i) {
-        if (has_dy) put_transposed(ry, kTerms<DT> == 1 ? 0 : i / tiles, ly[i & 1] + yt * BN + yl, BN / 8);
+    auto put_dy = [&](uint32_t i, uint32_t buf) {
+        if (has_dy) put_transposed(ry, kTerms<DT> == 1 ? 0 : i / tiles, ly[buf] + yt * BN + yl, BN / 8);
     };
-    auto put_x = [&](uint32_t i) {
-        if (has_x) put_transposed(rx, 0, lx[i & 1] + xt * BK + xl, BK / 8);
+    auto put_x = [&](uint32_t buf) {
+        if (has_x) put_transposed(rx, 0, lx[buf] + xt * BK + xl, BK / 8);
     };
 
     f32x16 acc[FN][FK];
@@ -281,46 +320,72 @@ __global__ __launch_bounds__(WN *WK *kWave, 1) void wgrad_kernel(const typename 
                 for (uint32_t j = 0; j < FK; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[which][i], fb[which][j], acc[i][j], 0, 0, 0);
         };
-        load(0);
-        put_dy(0);
+        // Multiplies tile i out of LDS buffer P, puts tile i + 1 into the other
+        // one and loads tile i + 2.  The barrier stands before the last quarter
+        // of the products: by then the other waves' pieces of tile i + 1 are
+        // in LDS, and its first fragments arrive behind those products.
+        auto step = [&](auto parity, uint32_t i) {
+            constexpr uint32_t P = decltype(parity)::value, Q = P ^ 1;
+            mend(i + 1);
+            read(1, P, 1);
+            put_dy(i + 1, Q);
+            multiply(0);
+            load_dy(i + 2);
+            read(0, P, 2);
+            put_x(Q);
+            multiply(1);
+            load_x(i + 2);
+            read(1, P, 3);
+            multiply(0);
+            interleave<FN * FK>();
+            lds_barrier();
+            read(0, Q, 0);
+            multiply(1);
+            interleave_tail<FN * FK, FN + FK>();
+        };
+        load_dy(0);
+        load_x(0);
+        mend(0);
+        put_dy(0, 0);
         put_x(0);
-        load(1);
+        load_dy(1);
+        load_x(1);
         lds_barrier();
         read(0, 0, 0);
-        for (uint32_t i = 0; i < steps; ++i) {
-            const uint32_t buf = i & 1;
-            read(1, buf, 1);
-            put_dy(i + 1);
-            multiply(0);
-            read(0, buf, 2);
-            put_x(i + 1);
-            multiply(1);
-            read(1, buf, 3);
-            load(i + 2);
-            multiply(0);
-            lds_barrier();
-            read(0, buf ^ 1, 0);
-            multiply(1);
+        for (uint32_t i = 0; i < steps; i += 2) {
+            step(std::integral_constant<uint32_t, 0>(), i);
+            if (i + 1 < steps) step(std::integral_constant<uint32_t, 1>(), i + 1);
         }
     }
 
     const uint32_t r0 = lane % 32;
     const uint64_t k = k0 + r0 % (BK / 8) * 8 + column_in_block<BK, FK>(wk, 0, r0);
+    auto write = [&](auto o) {
+        typedef typename Plain<decltype(o)::value>::type T;
+        T *base = static_cast<T *>(out) + (uint64_t)blockIdx.y * s.n * s.k;  // a slice's partial sums (one slice: the output)
 #pragma unroll
-    for (uint32_t i = 0; i < FN; ++i)
+        for (uint32_t i = 0; i < FN; ++i)
 #pragma unroll
-        for (uint32_t v = 0; v < 16; ++v) {
-            const uint32_t r = v / 4 * 8 + lane / 32 * 4 + v % 4;
-            const uint64_t n = n0 + r % (BN / 8) * 8 + column_in_block<BN, FN>(wn, i, r);
-            if (n >= s.n) continue;
-            typename Plain<ODT>::type *p = out + n * s.ld_out + k;
+            for (uint32_t v = 0; v < 16; ++v) {
+                const uint32_t r = v / 4 * 8 + lane / 32 * 4 + v % 4;
+                const uint64_t n = n0 + r % (BN / 8) * 8 + column_in_block<BN, FN>(wn, i, r);
+                if (n >= s.n) continue;
+                T *p = base + n * s.ld_out + k;
+                if (k + FK <= s.k && !add) {
+                    typedef T vec __attribute__((ext_vector_type(FK)));
+                    typedef vec any __attribute__((aligned(sizeof(T))));
+                    vec u;
 #pragma unroll
-            for (uint32_t j = 0; j < FK; ++j)
-                if (k + j < s.k) {
-                    const float old = add ? widen(p[j]) : 0.0f;
-                    p[j] = (typename Plain<ODT>::type)(acc[i][j][v] + old);
+                    for (uint32_t j = 0; j < FK; ++j) u[j] = (T)acc[i][j][v];
+                    *reinterpret_cast<any *>(p) = u;
+                } else {
+#pragma unroll
+                    for (uint32_t j = 0; j < FK; ++j)
+                        if (k + j < s.k) p[j] = (T)(acc[i][j][v] + (add ? widen(p[j]) : 0.0f));
                 }
-        }
+            }
+    };
+    with_dtype(out_dtype, write);
 }
 
 // Joins the slices' partial sums, in their order.
@@ -372,22 +437,23 @@ hipError_t launch_q8_weight_grad(const void *dy, int dtype, uint64_t ld_dy, uint
     const dim3 grid(s.tiles_n * s.tiles_k, p.slices);
     with_dtype(dtype, [&](auto d) {
         constexpr int DT = decltype(d)::value;
-        with_dtype(split ? (int)PC_F32 : dw_dtype, [&](auto o) {
-            constexpr int ODT = decltype(o)::value;
-            auto launch = [&](auto kern) {
-                hipLaunchKernelGGL(kern, grid, dim3(kThreads), 0, stream,
-                                   static_cast<const typename Plain<DT>::type *>(dy), x->sym, x->scale, s,
-                                   static_cast<typename Plain<ODT>::type *>(split ? ws : dw),
-                                   (uint32_t)(accumulate && !split));
-            };
-            auto by_format = [&](auto f) {
-                constexpr int FMT = decltype(f)::value;
-                p.side == 256 ? launch(wgrad_kernel<DT, FMT, ODT, 2, 2, 4, 4>)
-                              : launch(wgrad_kernel<DT, FMT, ODT, 2, 2, 2, 2>);
-            };
-            if (x->format == PC_Q8_E4M3) by_format(std::integral_constant<int, PC_Q8_E4M3>());
-            else by_format(std::integral_constant<int, PC_Q8_INT8>());
-        });
+        auto launch = [&](auto kern) {
+            hipLaunchKernelGGL(kern, grid, dim3(kThreads), 0, stream, static_cast<const typename Plain<DT>::type *>(dy),
+                               x->sym, x->scale, s, split ? ws : dw, split ? (int)PC_F32 : dw_dtype,
+                               (uint32_t)(accumulate && !split));
+        };
+        auto by_side = [&](auto f, auto r) {
+            constexpr int FMT = decltype(f)::value;
+            constexpr bool RAGGED = decltype(r)::value;
+            p.side == 256 ? launch(wgrad_kernel<DT, FMT, RAGGED, 2, 2, 4, 4>)
+                          : launch(wgrad_kernel<DT, FMT, RAGGED, 2, 2, 2, 2>);
+        };
+        auto by_format = [&](auto r) {
+            if (x->format == PC_Q8_E4M3) by_side(std::integral_constant<int, PC_Q8_E4M3>(), r);
+            else by_side(std::integral_constant<int, PC_Q8_INT8>(), r);
+        };
+        if (n % 8 || k % 8) by_format(std::true_type());
+        else by_format(std::false_type());
     });
     if (split)
         with_dtype(dw_dtype, [&](auto o) {

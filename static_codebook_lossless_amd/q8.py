@@ -65,13 +65,20 @@ def _same_device(a, b, what):
         raise ValueError("%s is on %s, not on %s" % (what, b.device, a.device))
 
 
+# the current stream's handle without the Stream object that
+# torch.cuda.current_stream builds around it (2 us of a 9 us call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch(what, device, fn, *args):
     """Call ``fn`` on the device's current stream."""
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            st = fn(*args, _raw_stream(index))
     if st:
         _check(st, what)
 
@@ -107,6 +114,14 @@ class Q8:
         self.symbols, self.scales, self.format = symbols, scales, format
         self.arg = StoredArg(symbols.data_ptr(), scales.data_ptr(), rows, cols, ld, ld_scale, code, 0)
 
+    @classmethod
+    def _dense(cls, symbols, scales, format, rows, cols, code):
+        """A stored tensor of two dense tensors just allocated for it."""
+        q = cls.__new__(cls)
+        q.symbols, q.scales, q.format = symbols, scales, format
+        q.arg = StoredArg(symbols.data_ptr(), scales.data_ptr(), rows, cols, cols, -(-cols // PC_Q8_GROUP), code, 0)
+        return q
+
     @property
     def shape(self):
         return self.symbols.shape
@@ -140,11 +155,13 @@ def pc_q8_store(x, format="e4m3", counts=None) -> Q8:
         if counts.dtype != torch.int64 or counts.shape != (256,) or not counts.is_contiguous():
             raise TypeError("counts must be 256 contiguous int64")
         _same_device(x, counts, "counts")
-    symbols = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((rows, -(-cols // PC_Q8_GROUP)), dtype=torch.uint8, device=x.device)
-    _launch("pc_q8_store", x.device, lib.pc_q8_store, x.data_ptr(), kind, rows, cols, ld, code, symbols.data_ptr(),
-            scales.data_ptr(), None if counts is None else counts.data_ptr())
-    return Q8(symbols, scales, format)
+    device = x.device
+    symbols = torch.empty((rows, cols), dtype=torch.uint8, device=device)
+    scales = torch.empty((rows, -(-cols // PC_Q8_GROUP)), dtype=torch.uint8, device=device)
+    q = Q8._dense(symbols, scales, format, rows, cols, code)
+    _launch("pc_q8_store", device, lib.pc_q8_store, x.data_ptr(), kind, rows, cols, ld, code, q.arg.sym, q.arg.scale,
+            None if counts is None else counts.data_ptr())
+    return q
 
 
 def _output(out, shape, dtype, device, what="out"):
@@ -332,8 +349,8 @@ def pc_embed_backward(dy, tokens, vocab, scale=1.0, dtype=torch.float32, padding
         raise ValueError("vocab is negative")
     out, ld_out = _output(out, (vocab, dim), dtype, dy.device)
     need = lib.pc_embed_backward_workspace_bytes(n, dim, vocab)
-    ws = torch.empty(need, dtype=torch.uint8, device=dy.device)
+    ws = torch.empty(need, dtype=torch.uint8, device=dy.device) if need else None
     _launch("pc_embed_backward", dy.device, lib.pc_embed_backward, dy.data_ptr(), kind, ld, tokens.data_ptr(),
             tokens.element_size(), n, dim, vocab, padding, scale, out.data_ptr(), out_kind, ld_out, int(accumulate),
-            ws.data_ptr(), need)
+            None if ws is None else ws.data_ptr(), need)
     return out

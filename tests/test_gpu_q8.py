@@ -494,7 +494,7 @@ def test_embed_backward(dtype, odt):
 def test_embed_backward_larger():
     # vocabularies of several ranges, more tokens than one pass of a workgroup, on the device in 64 bits
     g = torch.Generator(device=DEV).manual_seed(3)
-    for n, dim, vocab, skew in [(5000, 96, 20000, 1), (40000, 64, 50257, 6), (20000, 40, 300000, 3),
+    for n, dim, vocab, skew in [(1024, 520, 200000, 1), (1025, 520, 9000, 6), (5000, 96, 20000, 1), (40000, 64, 50257, 6), (20000, 40, 300000, 3),
                                 (70000, 16, 1000, 1)]:
         say("embed backward", n, dim, vocab)
         u = torch.rand(n, generator=g, device=DEV, dtype=torch.float64)
@@ -506,6 +506,8 @@ def test_embed_backward_larger():
         terms = torch.bincount(tokens, minlength=vocab).unsqueeze(1)
         assert bool((torch.abs(got.double() - want) <= (terms + 3) * 2.0 ** -23 * size).all())
         assert torch.equal(got, pc.pc_embed_backward(dy, tokens, vocab))
+        pc.pc_embed_backward(dy, tokens, vocab, out=got, accumulate=True)
+        assert bool((torch.abs(got.double() - 2 * want) <= (2 * terms + 6) * 2.0 ** -23 * size).all())
 
 
 def test_embed_backward_of_nothing_and_views():

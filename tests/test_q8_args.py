@@ -120,14 +120,14 @@ def test_embed_sizes():
 
 
 @pytest.mark.parametrize("kw", [dict(dy=None), dict(tok=None), dict(tb=3), dict(tok=A + 4), dict(dtype=9), dict(odt=9),
-                                dict(ld=63), dict(ldg=63), dict(grad=None), dict(ws=None), dict(ws=A + 8)])
+                                dict(ld=63), dict(ldg=63), dict(grad=None), dict(n=5000, ws=None), dict(n=5000, ws=A + 8)])
 def test_embed_backward_refuses(kw):
     assert back(**kw) == BAD
 
 
 def test_embed_backward_sizes():
-    need = pc.pc_embed_backward_workspace_bytes(5, 64, 10)
-    assert back(wsb=need - 1) == SMALL
+    need = pc.pc_embed_backward_workspace_bytes(5000, 64, 10)
+    assert back(n=5000, wsb=need - 1) == SMALL
     assert back(n=1 << 31) == BIG and back(vocab=(1 << 31) + 1) == BIG
     assert back(n=0, acc=1, dy=None, tok=None) == OK
     assert back(vocab=0, grad=None) == OK and back(dim=0, grad=None) == OK
