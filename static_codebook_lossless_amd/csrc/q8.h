@@ -38,36 +38,55 @@ __device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ float widen(_Float16 v) { return (float)v; }
 __device__ __forceinline__ float widen(__bf16 v) { return as_f32((uint32_t)__builtin_bit_cast(uint16_t, v) << 16); }
 
+// n (0..8) elements as loaded; the others 0.
+template <int DT> struct RawUnit { u32x4 w[DT == PC_F32 ? 2 : 1]; };
+
+template <int DT>
+__device__ __forceinline__ RawUnit<DT> load_raw(const typename Plain<DT>::type *p, uint32_t n) {
+    RawUnit<DT> r = {};
+    if (n == kUnit) {
+        if constexpr (DT == PC_F32) {
+            r.w[0] = *reinterpret_cast<const u32x4_any4 *>(p);
+            r.w[1] = *reinterpret_cast<const u32x4_any4 *>(p + 4);
+        } else {
+            r.w[0] = *reinterpret_cast<const u32x4_any2 *>(p);
+        }
+    } else if (n) {
+#pragma unroll
+        for (uint32_t i = 0; i < kUnit; ++i)
+            if (i < n) {
+                if constexpr (DT == PC_F32) r.w[i / 4][i % 4] = as_u32(p[i]);
+                else r.w[0][i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, p[i]) << (16 * (i % 2));
+            }
+    }
+    return r;
+}
+
+template <int DT>
+__device__ __forceinline__ void widen_unit(const RawUnit<DT> &r, float v[8]) {
+    if constexpr (DT == PC_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = as_f32(r.w[i / 4][i % 4]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t u = r.w[0][i];
+            if constexpr (DT == PC_BF16) {
+                v[2 * i] = as_f32(u << 16);
+                v[2 * i + 1] = as_f32(u & 0xFFFF0000u);
+            } else {
+                const f16x2 h = __builtin_bit_cast(f16x2, u);
+                v[2 * i] = (float)h[0];
+                v[2 * i + 1] = (float)h[1];
+            }
+        }
+    }
+}
+
 // n (1..8) elements at p as f32; the others 0.
 template <int DT>
 __device__ __forceinline__ void load_unit(const typename Plain<DT>::type *p, uint32_t n, float v[8]) {
-    if (n == kUnit) {
-        if constexpr (DT == PC_F32) {
-            const u32x4 a = *reinterpret_cast<const u32x4_any4 *>(p), b = *reinterpret_cast<const u32x4_any4 *>(p + 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = as_f32(a[i]);
-                v[4 + i] = as_f32(b[i]);
-            }
-        } else {
-            const u32x4 a = *reinterpret_cast<const u32x4_any2 *>(p);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (DT == PC_BF16) {
-                    v[2 * i] = as_f32(a[i] << 16);
-                    v[2 * i + 1] = as_f32(a[i] & 0xFFFF0000u);
-                } else {
-                    const uint32_t u = a[i];
-                    const f16x2 h = __builtin_bit_cast(f16x2, u);
-                    v[2 * i] = (float)h[0];
-                    v[2 * i + 1] = (float)h[1];
-                }
-            }
-        }
-    } else {
-#pragma unroll
-        for (uint32_t i = 0; i < kUnit; ++i) v[i] = i < n ? widen(p[i]) : 0.0f;
-    }
+    widen_unit<DT>(load_raw<DT>(p, n), v);
 }
 
 // A vector store at an address of a smaller alignment; STREAM: the caches need

@@ -23,13 +23,13 @@ constexpr uint32_t kTile = kThreads * kPerLane;
 // ---------------------------------------------------------------------------
 
 // Histogram of the symbols in LDS, as in the byte histogram but with 8 copies
-// per wave, 257 words apart, added to the caller's counts at the end.  33 KB
-// a workgroup, so that four fit a CU: with 16 copies and two workgroups the
-// loads of 64 Mi bf16 elements waited (89 us; 67 us with 8).
+// per wave, 257 words apart, added to the caller's counts at the end.
 constexpr uint32_t kCopies = 8;
 constexpr uint32_t kCopyStride = 257;
-constexpr uint32_t kBins = kThreads / kWave * kCopies * kCopyStride;
-constexpr uint32_t kCountBlocks = 1024;
+constexpr uint32_t kCountThreads = 1024;
+constexpr uint32_t kBins = kCountThreads / kWave * kCopies * kCopyStride;
+constexpr uint32_t kCountBlocks = 256;
+constexpr uint32_t kCountPerLane = 2;
 
 __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
     v = max(v, dpp_u32<0xB1>(v));  // neighbour in the pair
@@ -78,77 +78,106 @@ __device__ __forceinline__ u32x2 with_nan(u32x2 w, uint32_t bad) {
     return w;
 }
 
+// PER units in a lane; the next tile's are loaded while a tile is stored and
+// counted (a counting workgroup takes many tiles, the others one).
 template <int DT, int FMT, bool COUNT>
-__global__ __launch_bounds__(kThreads) void store_kernel(const typename Plain<DT>::type *__restrict__ x, Units units,
+__global__ __launch_bounds__(COUNT ? kCountThreads : kThreads) void store_kernel(const typename Plain<DT>::type *__restrict__ x, Units units,
                                                          uint64_t ldx, uint64_t ld_sym, uint64_t ld_scale,
                                                          uint8_t *__restrict__ sym, uint8_t *__restrict__ scale,
                                                          uint64_t *__restrict__ counts) {
+    constexpr uint32_t THREADS = COUNT ? kCountThreads : kThreads, PER = COUNT ? kCountPerLane : kPerLane;
+    constexpr uint32_t kTileUnits = THREADS * PER;
     __shared__ uint32_t bins[COUNT ? kBins : 1];
     const uint32_t tid = threadIdx.x;
     uint32_t *my = bins;
-    if constexpr (COUNT) {
-        for (uint32_t i = tid; i < kBins; i += kThreads) bins[i] = 0;
-        __syncthreads();
-        my += ((tid / kWave) * kCopies + (tid % kWave) / (kWave / kCopies)) * kCopyStride;
-    }
-    for (uint64_t base = (uint64_t)blockIdx.x * kTile; base < units.total; base += (uint64_t)gridDim.x * kTile) {
-        float v[kPerLane][8];
-        uint64_t row[kPerLane], col[kPerLane];
-        uint32_t n[kPerLane];
+    struct Unit {
+        RawUnit<DT> raw;
+        uint64_t row, col;
+        uint32_t n;
+    };
+    auto load = [&](uint64_t base, Unit u[PER]) {
 #pragma unroll
-        for (uint32_t j = 0; j < kPerLane; ++j) {
-            const uint32_t local = j * kThreads + tid;
-            n[j] = 0;
-            row[j] = col[j] = 0;
+        for (uint32_t j = 0; j < PER; ++j) {
+            const uint32_t local = j * THREADS + tid;
+            u[j].n = 0;
+            u[j].row = u[j].col = 0;
             if (base + local < units.total) {
-                find_unit(units, base, local, row[j], col[j]);
+                find_unit(units, base, local, u[j].row, u[j].col);
                 // a short group's last units may hold no column at all
-                if (col[j] < units.cols) n[j] = (uint32_t)min((uint64_t)kUnit, units.cols - col[j]);
+                if (u[j].col < units.cols) u[j].n = (uint32_t)min((uint64_t)kUnit, units.cols - u[j].col);
             }
-            if (n[j]) {
-                load_unit<DT>(x + row[j] * ldx + col[j], n[j], v[j]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
-            }
+            u[j].raw = load_raw<DT>(x + u[j].row * ldx + u[j].col, u[j].n);
         }
+    };
+    auto store = [&](const Unit &u) {
+        float v[8];
+        widen_unit<DT>(u.raw, v);
+        uint32_t top = 0, bad = 0;
 #pragma unroll
-        for (uint32_t j = 0; j < kPerLane; ++j) {
-            uint32_t top = 0, bad = 0;
+        for (int i = 0; i < 8; ++i) top = max(top, as_u32(v[i]) & 0x7FFFFFFFu);
+        if (top >= 0x7F800000u) {  // infinities and NaN take no part
+            top = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = max(top, as_u32(v[j][i]) & 0x7FFFFFFFu);
-            if (top >= 0x7F800000u) {  // infinities and NaN take no part
-                top = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t u = as_u32(v[j][i]) & 0x7FFFFFFFu;
-                    if (u >= 0x7F800000u) {
-                        bad |= 1u << i;
-                        v[j][i] = 0.0f;
-                    } else {
-                        top = max(top, u);
-                    }
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t a = as_u32(v[i]) & 0x7FFFFFFFu;
+                if (a >= 0x7F800000u) {
+                    bad |= 1u << i;
+                    v[i] = 0.0f;
+                } else {
+                    top = max(top, a);
                 }
             }
-            const uint32_t code = code_for<FMT>(quad_max(top));
-            u32x2 w = to_symbols<FMT>(v[j], as_f32((254 - code) << 23));
-            if (bad) w = with_nan<FMT>(w, bad);
-            if (n[j]) {
-                store_symbols(sym + row[j] * ld_sym + col[j], n[j], w);
-                if (col[j] % kGroup == 0) scale[row[j] * ld_scale + col[j] / kGroup] = (uint8_t)code;
-            }
-            if constexpr (COUNT) {
+        }
+        const uint32_t code = code_for<FMT>(quad_max(top));
+        u32x2 w = to_symbols<FMT>(v, as_f32((254 - code) << 23));
+        if (bad) w = with_nan<FMT>(w, bad);
+        if (u.n) {
+            store_symbols(sym + u.row * ld_sym + u.col, u.n, w);
+            if (u.col % kGroup == 0) scale[u.row * ld_scale + u.col / kGroup] = (uint8_t)code;
+        }
+        if constexpr (COUNT) {
+            if (u.n == kUnit) {
+#pragma unroll
+                for (uint32_t i = 0; i < kUnit; ++i) atomicAdd(&my[(w[i / 4] >> (8 * (i % 4))) & 0xFF], 1u);
+            } else {
 #pragma unroll
                 for (uint32_t i = 0; i < kUnit; ++i)
-                    if (i < n[j]) atomicAdd(&my[(w[i / 4] >> (8 * (i % 4))) & 0xFF], 1u);
+                    if (i < u.n) atomicAdd(&my[(w[i / 4] >> (8 * (i % 4))) & 0xFF], 1u);
             }
         }
-    }
-    if constexpr (COUNT) {
+    };
+    Unit u[PER];
+    uint64_t base = (uint64_t)blockIdx.x * kTileUnits;
+    load(base, u);
+    if constexpr (!COUNT) {
+#pragma unroll
+        for (uint32_t j = 0; j < PER; ++j) store(u[j]);
+    } else {
+        for (uint32_t i = tid; i < kBins; i += THREADS) bins[i] = 0;
         __syncthreads();
-        uint64_t s = 0;
-        for (uint32_t c = 0; c < kThreads / kWave * kCopies; ++c) s += bins[c * kCopyStride + tid];
-        if (s) atomicAdd(reinterpret_cast<unsigned long long *>(&counts[tid]), (unsigned long long)s);
+        my += ((tid / kWave) * kCopies + (tid % kWave) / (kWave / kCopies)) * kCopyStride;
+        for (; base < units.total; base += (uint64_t)gridDim.x * kTileUnits) {
+            Unit next[PER];
+            load(base + (uint64_t)gridDim.x * kTileUnits, next);
+#pragma unroll
+            for (uint32_t j = 0; j < PER; ++j) store(u[j]);
+#pragma unroll
+            for (uint32_t j = 0; j < PER; ++j) u[j] = next[j];
+        }
+        __syncthreads();
+        // four threads a bin, a quarter of the copies each
+        constexpr uint32_t kShare = THREADS / 256;
+        uint32_t s = 0;
+        for (uint32_t c = tid / 256; c < THREADS / kWave * kCopies; c += kShare) s += bins[c * kCopyStride + tid % 256];
+        __syncthreads();
+        bins[tid] = s;
+        __syncthreads();
+        if (tid < 256) {
+            uint64_t sum = 0;
+#pragma unroll
+            for (uint32_t c = 0; c < kShare; ++c) sum += bins[c * 256 + tid];
+            if (sum) atomicAdd(reinterpret_cast<unsigned long long *>(&counts[tid]), (unsigned long long)sum);
+        }
     }
 }
 
@@ -321,13 +350,14 @@ bool dense(const pc_q8 *q) { return q->ld_sym == q->cols && q->ld_scale * kGroup
 hipError_t launch_q8_store(const void *x, int dtype, uint64_t rows, uint64_t cols, uint64_t ldx, int format,
                            uint8_t *sym, uint8_t *scale, uint64_t *counts, hipStream_t stream) {
     const Units units = make_units(rows, cols, ldx == cols);
-    const uint64_t groups = (cols + kGroup - 1) / kGroup, tiles = (units.total + kTile - 1) / kTile;
+    const uint64_t groups = (cols + kGroup - 1) / kGroup;
+    const uint64_t tile = counts ? kCountThreads * kCountPerLane : kTile, tiles = (units.total + tile - 1) / tile;
     const dim3 grid((uint32_t)(counts ? std::min<uint64_t>(tiles, kCountBlocks) : tiles));
     with_dtype(dtype, [&](auto d) {
         constexpr int DT = decltype(d)::value;
         typedef const typename Plain<DT>::type *P;
         auto launch = [&](auto k) {
-            hipLaunchKernelGGL(k, grid, dim3(kThreads), 0, stream, static_cast<P>(x), units, ldx, cols, groups, sym,
+            hipLaunchKernelGGL(k, grid, dim3(counts ? kCountThreads : kThreads), 0, stream, static_cast<P>(x), units, ldx, cols, groups, sym,
                                scale, counts);
         };
         if (format == PC_Q8_E4M3)
