@@ -24,23 +24,18 @@ constexpr uint32_t kStep = 64;  // rows t of one LDS tile
 // bits, f32 (24 bits) three.
 template <int DT> constexpr uint32_t kTerms = DT == PC_BF16 ? 1 : DT == PC_F16 ? 2 : 3;
 
-// Term `which` of v, as the upper half of an f32: v cut off to 8 bits, then
+// Term `WHICH` of v, as the upper half of an f32: v cut off to 8 bits, then
 // what is left, which 32 bits hold exactly.  Infinity and NaN are their own
 // first term and leave 0.
-__device__ __forceinline__ float cut(float v) {
-    const uint32_t u = as_u32(v), special = (u & 0x7FFFFFFFu) > 0x7F800000u ? 0x400000u : 0u;  // NaN stays NaN
-    return as_f32((u | special) & 0xFFFF0000u);
-}
-__device__ __forceinline__ float left(float v, float first) {
-    return (as_u32(v) & 0x7F800000u) == 0x7F800000u ? 0.0f : v - first;
-}
-__device__ __forceinline__ uint32_t term_bits(float v, uint32_t which) {
-    float t = cut(v);
-    for (uint32_t i = 0; i < which; ++i) {
-        v = left(v, t);
-        t = cut(v);
+template <uint32_t WHICH>
+__device__ __forceinline__ uint32_t term_bits(float v) {
+    const uint32_t u = as_u32(__builtin_canonicalizef(v));  // a NaN's upper half is one too
+    if constexpr (WHICH == 0) {
+        return u;
+    } else {
+        const float rest = v - as_f32(u & 0xFFFF0000u);
+        return term_bits<WHICH - 1>(__builtin_isfinite(v) ? rest : 0.0f);
     }
-    return as_u32(t);
 }
 
 // Memory as the hardware's bounds-checked buffer: a load that starts at or
@@ -59,9 +54,9 @@ struct Window {
         const uint32_t bytes = high < 0 ? 0u : high > 0 ? 0xFFFFFFFFu : (uint32_t)left;
         return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(at), 0, (int)bytes, 0x00020000);
     }
-    __device__ __forceinline__ void down() {
-        at += step;
-        left -= (int64_t)step;
+    __device__ __forceinline__ void down(uint32_t tiles = 1) {
+        at += tiles * step;
+        left -= (int64_t)(tiles * step);
     }
 };
 
@@ -90,8 +85,9 @@ template <int DT, uint32_t P> struct RawDy {
             }
         }
     }
-    // piece p in bf16
-    __device__ __forceinline__ u32x4 piece(uint32_t p, uint32_t which) const {
+    // piece p's term in bf16
+    template <uint32_t WHICH>
+    __device__ __forceinline__ u32x4 piece(uint32_t p) const {
         if constexpr (DT == PC_BF16) {
             return w[p][0];
         } else {
@@ -108,7 +104,7 @@ template <int DT, uint32_t P> struct RawDy {
                     a = as_f32(w[p][k / 2][(2 * k) % 4]);
                     b = as_f32(w[p][k / 2][(2 * k) % 4 + 1]);
                 }
-                out[k] = __builtin_amdgcn_perm(term_bits(b, which), term_bits(a, which), 0x07060302u);
+                out[k] = __builtin_amdgcn_perm(term_bits<WHICH>(b), term_bits<WHICH>(a), 0x07060302u);
             }
             return out;
         }
@@ -145,24 +141,15 @@ template <int FMT, uint32_t P> struct RawX {
                 out[2 * k + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[p][2 * h + k], s, true));
             }
         } else {
-            float v[8];
-            const u32x2 u = {w[p][2 * h], w[p][2 * h + 1]};
-            // one multiply-add a symbol where 128 times the scale is a number and no symbol NaN
-            const uint32_t a = u[0] ^ 0x80808080u, b = u[1] ^ 0x80808080u;
-            const bool nan = (((a - 0x01010101u) & ~a) | ((b - 0x01010101u) & ~b)) & 0x80808080u;
-            if (nan || code[p] > 247) {
-                unit_values<FMT>(u, s, v);
-            } else {
-                const float down = -128.0f * s;
+            // without branches, in the middle of the products
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    v[k] = __builtin_fmaf((float)((a >> (8 * k)) & 0xFFu), s, down);
-                    v[4 + k] = __builtin_fmaf((float)((b >> (8 * k)) & 0xFFu), s, down);
-                }
+            for (uint32_t k = 0; k < 4; ++k) {
+                const uint32_t u = w[p][2 * h + k / 2] >> (16 * (k % 2));
+                float lo = (float)(int)(int8_t)(u & 0xFFu), hi = (float)(int)(int8_t)((u >> 8) & 0xFFu);
+                lo = lo == -128.0f ? __builtin_nanf("") : lo;
+                hi = hi == -128.0f ? __builtin_nanf("") : hi;
+                out[k] = __builtin_amdgcn_perm(as_u32(hi * s), as_u32(lo * s), 0x07060302u);
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                out[k] = __builtin_amdgcn_perm(as_u32(v[2 * k + 1]), as_u32(v[2 * k]), 0x07060302u);
         }
         return out;
     }
@@ -231,6 +218,23 @@ __device__ __forceinline__ void interleave() {
     }
 }
 
+// Three phases as one where the pieces take much vector work (int8, terms of
+// f16 and f32): 8 vector instructions behind each of the 48 matrix instructions.
+template <uint32_t M>
+__device__ __forceinline__ void interleave_three() {
+    if constexpr (M == 16) {
+#pragma unroll
+        for (uint32_t m = 0; m < 48; ++m) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 8, 0);
+            if (m % 3 == 2) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+            if (m >= 32) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
 // SETS: tiles on their way in registers.
 template <int DT, int FMT, bool RAGGED, uint32_t WN, uint32_t WK, uint32_t FN, uint32_t FK, uint32_t SETS>
 __global__ __launch_bounds__(WN *WK *kWave, FN * FK == 16 ? 1 : 2) void wgrad_kernel(const typename Plain<DT>::type *__restrict__ dy,
@@ -252,7 +256,6 @@ __global__ __launch_bounds__(WN *WK *kWave, FN * FK == 16 ? 1 : 2) void wgrad_ke
     const uint64_t n0 = (uint64_t)tile.n * BN, k0 = (uint64_t)tile.k * BK;
     const uint32_t all = (uint32_t)((s.t + kStep - 1) / kStep);
     const uint32_t first = min(all, blockIdx.y * s.slice), tiles = min(all - first, s.slice);
-    const uint32_t steps = tiles * kTerms<DT>;
 
     const uint32_t yc = tid % UN, yt = tid / UN, xc = tid % (UK / 2), xt = tid / (UK / 2);  // first pieces
     const uint32_t y_row = (uint32_t)s.ld_dy * kElem, x_row = (uint32_t)s.ld_sym, c_row = (uint32_t)s.ld_scale;
@@ -269,74 +272,34 @@ __global__ __launch_bounds__(WN *WK *kWave, FN * FK == 16 ? 1 : 2) void wgrad_ke
     const Window x0(sym + k0, x_row, t_first * x_row, rows, s.k - k0);
     const Window q0(scale + c0, c_row, t_first * c_row, rows, (s.k + kGroup - 1) / kGroup - c0);
     Window yw = y0, xw = x0, qw = q0;
-    uint32_t y_tile = 0, x_tile = 0;  // for gradients of several terms, which read dy and x once for each
     auto load_dy = [&](RawDy<DT, PY> &r) {
         r.load(yw.buffer(), y_at, RY * y_row);
         yw.down();
-        if (kTerms<DT> > 1 && ++y_tile == tiles) {
-            y_tile = 0;
-            yw = y0;
-        }
     };
     auto load_x = [&](RawX<FMT, PX> &r) {
         r.load(xw.buffer(), x_at, RX * x_row, qw.buffer(), c_at, RX * c_row);
         xw.down();
         qw.down();
-        if (kTerms<DT> > 1 && ++x_tile == tiles) {
-            x_tile = 0;
-            xw = x0;
-            qw = q0;
-        }
     };
-    // A piece that sticks out of the tensor's last row (widths that are no
-    // multiple of a piece): its load may have dropped elements that are inside.
-    // Only the last tiles of t meet one.
-    auto mend = [&](RawDy<DT, PY> &y, RawX<FMT, PX> &x, uint32_t i) {
-        if constexpr (!RAGGED) return;
-        const uint64_t t0 = (uint64_t)(kTerms<DT> == 1 ? i : i % tiles) * kStep;
-        if (i >= steps || rows - t0 >= kStep + 16) return;
-        const uint64_t cy = n0 + yc * 8, cx = k0 + xc * 16;
-        if (cy < s.n && cy + 8 > s.n) {
-            Window w = y0;
-            w.at += t0 * y_row;
-            w.left -= (int64_t)(t0 * y_row);
+    auto put_dy = [&](const RawDy<DT, PY> &r, auto which, uint32_t buf) {
+        u32x4 *to = ly[buf] + yt * UN + swizzled(yc, yt);
 #pragma unroll
-            for (uint32_t p = 0; p < PY; ++p) {
-                const uint32_t at = y_at + p * RY * y_row;
-                if (at < w.left && at + 8 * kElem > w.left) y.load_single(p, w.buffer(), at, (uint32_t)(s.n - cy));
-            }
-        }
-        if (cx < s.k && cx + 16 > s.k) {
-            Window w = x0;
-            w.at += t0 * x_row;
-            w.left -= (int64_t)(t0 * x_row);
-#pragma unroll
-            for (uint32_t p = 0; p < PX; ++p) {
-                const uint32_t at = x_at + p * RX * x_row;
-                if (at < w.left && at + 16 > w.left) x.load_single(p, w.buffer(), at, (uint32_t)(s.k - cx));
-            }
-        }
+        for (uint32_t p = 0; p < PY; ++p) to[p * RY * UN] = r.template piece<decltype(which)::value>(p);
     };
-    auto put_dy = [&](const RawDy<DT, PY> &r, uint32_t i) {
-        u32x4 *to = ly[i & 1] + yt * UN + swizzled(yc, yt);
-#pragma unroll
-        for (uint32_t p = 0; p < PY; ++p) to[p * RY * UN] = r.piece(p, kTerms<DT> == 1 ? 0 : i / tiles);
-    };
-    auto put_x = [&](const RawX<FMT, PX> &r, uint32_t i) {
-        u32x4 *to = lx[i & 1] + xt * UK + swizzled(2 * xc, xt);
+    auto put_x = [&](const RawX<FMT, PX> &r, uint32_t buf) {
+        u32x4 *to = lx[buf] + xt * UK + swizzled(2 * xc, xt);
 #pragma unroll
         for (uint32_t p = 0; p < PX; ++p)
 #pragma unroll
             for (uint32_t h = 0; h < 2; ++h) to[p * RX * UK + h] = r.piece(p, h);
     };
-
     f32x16 acc[FN][FK];
 #pragma unroll
     for (uint32_t i = 0; i < FN; ++i)
 #pragma unroll
         for (uint32_t j = 0; j < FK; ++j) acc[i][j] = f32x16{0};
 
-    if (steps) {
+    if (tiles) {
         // a lane's place in the transposing reads: row q (of 4) of the half
         // wave's 8, columns 16 (lane / 16 % 2) + 4 (lane % 4) of the fragment's 32
         const uint32_t q = lane % 16 / 4, row = lane / 32 * 8 + q, within = lane / 16 % 2 * 32 + lane % 4 * 8;
@@ -368,84 +331,200 @@ __global__ __launch_bounds__(WN *WK *kWave, FN * FK == 16 ? 1 : 2) void wgrad_ke
         // before the last quarter of the products: by then the other waves'
         // pieces of tile i + 1 are in LDS, and its first fragments arrive behind
         // those products.
-        auto step = [&](auto set, uint32_t i) {
+        auto step = [&](auto set, auto which, uint32_t i) {
             constexpr uint32_t R = decltype(set)::value, M = FN * FK;
+            constexpr bool kFewVector = FMT == PC_Q8_E4M3 && kTerms<DT> == 1;
             const uint32_t buf = i & 1;
-            mend(ry[R], rx[R], i + 1);
             read(1, buf, 1);
-            put_dy(ry[R], i + 1);
+            put_dy(ry[R], which, buf ^ 1);
             multiply(0);
-            interleave<M, 0, 8, 0>();
+            if (kFewVector) interleave<M, 0, 8, 0>();
             load_dy(ry[R]);
             read(0, buf, 2);
-            put_x(rx[R], i + 1);
+            put_x(rx[R], buf ^ 1);
             multiply(1);
-            interleave<M, 32, 8, 8, true>();
+            if (kFewVector) interleave<M, 32, 8, 8, true>();
             load_x(rx[R]);
             read(1, buf, 3);
             multiply(0);
-            interleave<M, 0, 0, 8>();
+            if (kFewVector) interleave<M, 0, 0, 8>();
+            else interleave_three<M>();
             lds_barrier();
             read(0, buf ^ 1, 0);
             multiply(1);
             interleave<M, 0, 0, 0>();
         };
-        auto run = [&](auto self, auto set, uint32_t i) {
+        auto run = [&](auto self, auto set, auto which, uint32_t i, uint32_t end) {
             constexpr uint32_t R = decltype(set)::value;
-            if (R && i >= steps) return;
-            step(std::integral_constant<uint32_t, (R + 1) % SETS>(), i);
-            if constexpr (R + 1 < SETS) self(self, std::integral_constant<uint32_t, R + 1>(), i + 1);
+            if (R && i >= end) return;
+            step(std::integral_constant<uint32_t, (R + 1) % SETS>(), which, i);
+            if constexpr (R + 1 < SETS) self(self, std::integral_constant<uint32_t, R + 1>(), which, i + 1, end);
         };
-        // tile 0 goes to LDS, tiles 1 .. SETS to the sets 1, .., SETS - 1, 0
-        load_dy(ry[0]);
-        load_x(rx[0]);
+        // Widths that are no multiple of a piece: a piece that sticks out of the
+        // tensor's last row may lose the elements that are inside, as its load
+        // crosses the end.  The tiles that can hold one (the last, and the one
+        // before where rows are shorter than a piece) are done by themselves.
+        const uint32_t apart = !RAGGED || rows > (uint64_t)tiles * kStep + 16 ? 0
+                               : rows + kStep > (uint64_t)tiles * kStep + 16 ? 1
+                                                                             : 2;
+        const uint32_t whole = tiles - min(tiles, apart);
+        auto pass = [&](auto which) {
+            yw = y0;
+            xw = x0;
+            qw = q0;
+            if (!RAGGED || whole) {
+                // tile 0 goes to LDS, tiles 1 .. SETS to the sets 1, .., SETS - 1, 0
+                load_dy(ry[0]);
+                load_x(rx[0]);
 #pragma unroll
-        for (uint32_t r = 1; r < SETS; ++r) {
-            load_dy(ry[r]);
-            load_x(rx[r]);
-        }
-        mend(ry[0], rx[0], 0);
-        put_dy(ry[0], 0);
-        put_x(rx[0], 0);
-        load_dy(ry[0]);
-        load_x(rx[0]);
-        lds_barrier();
-        read(0, 0, 0);
+                for (uint32_t r = 1; r < SETS; ++r) {
+                    load_dy(ry[r]);
+                    load_x(rx[r]);
+                }
+                put_dy(ry[0], which, 0);
+                put_x(rx[0], 0);
+                load_dy(ry[0]);
+                load_x(rx[0]);
+                lds_barrier();
+                read(0, 0, 0);
 #pragma unroll 1
-        for (uint32_t i = 0; i < steps; i += SETS) run(run, std::integral_constant<uint32_t, 0>(), i);
+                for (uint32_t i = 0; i < whole; i += SETS)
+                    run(run, std::integral_constant<uint32_t, 0>(), which, i, whole);
+            }
+            if constexpr (RAGGED) {
+#pragma unroll 1
+                for (uint32_t i = whole; i < tiles; ++i) {
+                    yw = y0;
+                    xw = x0;
+                    qw = q0;
+                    yw.down(i);
+                    xw.down(i);
+                    qw.down(i);
+                    const Window ye = yw, xe = xw;
+                    load_dy(ry[0]);
+                    load_x(rx[0]);
+                    const uint64_t cy = n0 + yc * 8, cx = k0 + xc * 16;
+                    if (cy < s.n && cy + 8 > s.n) {
+#pragma unroll
+                        for (uint32_t p = 0; p < PY; ++p) {
+                            const uint32_t at = y_at + p * RY * y_row;
+                            if (at < ye.left && at + 8 * kElem > ye.left)
+                                ry[0].load_single(p, ye.buffer(), at, (uint32_t)(s.n - cy));
+                        }
+                    }
+                    if (cx < s.k && cx + 16 > s.k) {
+#pragma unroll
+                        for (uint32_t p = 0; p < PX; ++p) {
+                            const uint32_t at = x_at + p * RX * x_row;
+                            if (at < xe.left && at + 16 > xe.left)
+                                rx[0].load_single(p, xe.buffer(), at, (uint32_t)(s.k - cx));
+                        }
+                    }
+                    lds_barrier();  // the other waves' reads of the last tile
+                    put_dy(ry[0], which, 0);
+                    put_x(rx[0], 0);
+                    lds_barrier();
+#pragma unroll
+                    for (uint32_t kk = 0; kk < kStep / 16; ++kk) {
+                        read(0, 0, kk);
+                        multiply(0);
+                    }
+                }
+            }
+        };
+        pass(std::integral_constant<uint32_t, 0>());
+        if constexpr (kTerms<DT> > 1) {
+            lds_barrier();  // the other waves' reads of the last tile
+            pass(std::integral_constant<uint32_t, 1>());
+        }
+        if constexpr (kTerms<DT> > 2) {
+            lds_barrier();
+            pass(std::integral_constant<uint32_t, 2>());
+        }
     }
 
+    const bool inside = n0 + BN <= s.n && k0 + BK <= s.k && !add;
     auto write = [&](auto o) {
         typedef typename Plain<decltype(o)::value>::type T;
-        T *base = static_cast<T *>(out) + (uint64_t)blockIdx.y * s.n * s.k;  // a slice's partial sums (one slice: the output)
+        // a slice's partial sums (one slice: the output), at the wave's first row and column, the same for all lanes
+        T *base = static_cast<T *>(out) + (uint64_t)blockIdx.y * s.n * s.k + (n0 + wn * FN * 32) * s.ld_out + k0 +
+                  wk * FK * 32;
+        const uint32_t below = lane / 32 * 4;
+        const uint64_t at = below * s.ld_out + lane % 32;
+        if (inside) {
+            // 128 bytes a row and half wave.  A large result in f32 streams past
+            // the caches (352 -> 342 us); partial sums, which only the small
+            // tiles leave, are read next.
+#pragma unroll
+            for (uint32_t i = 0; i < FN; ++i)
+#pragma unroll
+                for (uint32_t v = 0; v < 16; ++v) {
+                    T *p = base + (i * 32 + v / 4 * 8 + v % 4) * s.ld_out + at;
+#pragma unroll
+                    for (uint32_t j = 0; j < FK; ++j) {
+                        if constexpr (decltype(o)::value == PC_F32 && FN * FK == 16) {
+                            const float value = acc[i][j][v];
+                            __builtin_nontemporal_store(value, p + j * 32);
+                        } else {
+                            p[j * 32] = (T)acc[i][j][v];
+                        }
+                    }
+                }
+            return;
+        }
 #pragma unroll
         for (uint32_t i = 0; i < FN; ++i)
 #pragma unroll
             for (uint32_t v = 0; v < 16; ++v) {
-                const uint64_t n = n0 + (wn * FN + i) * 32 + v / 4 * 8 + lane / 32 * 4 + v % 4;
-                if (n >= s.n) continue;
+                const uint32_t r = i * 32 + v / 4 * 8 + v % 4;
+                if (n0 + wn * FN * 32 + r + below >= s.n) continue;
+                T *p = base + r * s.ld_out + at;
 #pragma unroll
-                for (uint32_t j = 0; j < FK; ++j) {
-                    const uint64_t k = k0 + (wk * FK + j) * 32 + lane % 32;
-                    T *p = base + n * s.ld_out + k;
-                    if (k < s.k) *p = (T)(acc[i][j][v] + (add ? widen(*p) : 0.0f));
-                }
+                for (uint32_t j = 0; j < FK; ++j)
+                    if (k0 + (wk * FK + j) * 32 + lane % 32 < s.k)
+                        p[j * 32] = (T)(acc[i][j][v] + (add ? widen(p[j * 32]) : 0.0f));
             }
     };
     with_dtype(out_dtype, write);
 }
 
-// Joins the slices' partial sums, in their order.
+// Joins the slices' partial sums, in their order: four neighbours of the dense
+// partial sums in a lane, whose loads for 8 slices are in flight together.
 template <int ODT>
 __global__ __launch_bounds__(kThreads) void join_kernel(const float *__restrict__ part, uint32_t slices, uint64_t n,
                                                         uint64_t k, uint64_t ld_out,
                                                         typename Plain<ODT>::type *__restrict__ out, uint32_t add) {
-    const uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= n * k) return;
-    float v = 0.0f;
-    for (uint32_t s = 0; s < slices; ++s) v += part[s * n * k + i];
-    typename Plain<ODT>::type *p = out + i / k * ld_out + i % k;
-    *p = (typename Plain<ODT>::type)(v + (add ? widen(*p) : 0.0f));
+    constexpr uint32_t kAhead = 8;
+    typedef typename Plain<ODT>::type T;
+    const uint64_t all = n * k, i = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+    if (i >= all) return;
+    const uint64_t at = min(i, all - min(all, (uint64_t)4));  // the last lane's four may start earlier
+    const uint32_t have = (uint32_t)min(all, (uint64_t)4);
+    f32x4 sum = {0, 0, 0, 0};
+    for (uint32_t s0 = 0; s0 < slices; s0 += kAhead) {
+        f32x4 v[kAhead];
+#pragma unroll
+        for (uint32_t a = 0; a < kAhead; ++a) {
+            const float *p = part + min(s0 + a, slices - 1) * all + at;
+            if (have == 4) {
+                typedef f32x4 any __attribute__((aligned(4)));
+                v[a] = *reinterpret_cast<const any *>(p);
+            } else {
+#pragma unroll
+                for (uint32_t j = 0; j < 4; ++j) v[a][j] = j < have ? p[j] : 0.0f;
+            }
+        }
+#pragma unroll
+        for (uint32_t a = 0; a < kAhead; ++a)
+            if (s0 + a < slices) sum += v[a];
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) {
+        const uint64_t e = at + j;
+        if (j >= have || e < i) continue;  // an earlier lane's
+        T *p = out + e / k * ld_out + e % k;
+        *p = (T)(sum[j] + (add ? widen(*p) : 0.0f));
+    }
 }
 
 // Tile sides: 256 (a wave's 128 x 128 part reads the least from LDS for each
@@ -462,7 +541,7 @@ Plan plan_of(uint64_t t, uint64_t n, uint64_t k) {
     p.side = tiles_of(n, k, 256) >= 192 ? 256 : 128;
     const uint64_t tiles = tiles_of(n, k, p.side);
     p.slices = 1;
-    if (tiles < 256 && steps >= 8) p.slices = (uint32_t)std::min<uint64_t>(512 / tiles, steps / 4);
+    if (p.side == 128 && tiles < 256 && steps >= 8) p.slices = (uint32_t)std::min<uint64_t>(512 / tiles, steps / 4);
     p.slice = (uint32_t)((steps + p.slices - 1) / p.slices);
     return p;
 }
@@ -505,7 +584,7 @@ hipError_t launch_q8_weight_grad(const void *dy, int dtype, uint64_t ld_dy, uint
     if (split)
         with_dtype(dw_dtype, [&](auto o) {
             constexpr int ODT = decltype(o)::value;
-            hipLaunchKernelGGL(join_kernel<ODT>, dim3((uint32_t)((n * k + kThreads - 1) / kThreads)), dim3(kThreads), 0,
+            hipLaunchKernelGGL(join_kernel<ODT>, dim3((uint32_t)((n * k + 4 * kThreads - 1) / (4 * kThreads))), dim3(kThreads), 0,
                                stream, static_cast<const float *>(ws), p.slices, n, k, ld_dw,
                                static_cast<typename Plain<ODT>::type *>(dw), (uint32_t)accumulate);
         });
