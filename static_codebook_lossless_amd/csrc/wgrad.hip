@@ -488,47 +488,57 @@ __global__ __launch_bounds__(WN *WK *kWave, FN * FK == 16 ? 1 : 2) void wgrad_ke
     with_dtype(out_dtype, write);
 }
 
-// Joins the slices' partial sums, in their order: four neighbours of the dense
-// partial sums in a lane, whose loads for 8 slices are in flight together.
+// Joins the slices' partial sums: four neighbours of the dense partial sums in
+// a lane, a quarter of the slices in each of the four waves, in their order,
+// the loads for 8 of them in flight together.
 template <int ODT>
 __global__ __launch_bounds__(kThreads) void join_kernel(const float *__restrict__ part, uint32_t slices, uint64_t n,
                                                         uint64_t k, uint64_t ld_out,
                                                         typename Plain<ODT>::type *__restrict__ out, uint32_t add) {
-    constexpr uint32_t kAhead = 8;
+    constexpr uint32_t kAhead = 8, kShares = kThreads / kWave;
     typedef typename Plain<ODT>::type T;
-    const uint64_t all = n * k, i = ((uint64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
-    if (i >= all) return;
-    const uint64_t at = min(i, all - min(all, (uint64_t)4));  // the last lane's four may start earlier
-    const uint32_t have = (uint32_t)min(all, (uint64_t)4);
+    __shared__ f32x4 sums[kShares][kWave];
+    const uint32_t lane = threadIdx.x % kWave, share = threadIdx.x / kWave;
+    const uint64_t all = n * k, i = ((uint64_t)blockIdx.x * kWave + lane) * 4;
+    const uint32_t have = i < all ? (uint32_t)min(all - i, (uint64_t)4) : 0;
+    const uint32_t each = (slices + kShares - 1) / kShares, first = min(slices, share * each);
+    const uint32_t end = min(slices, first + each);
     f32x4 sum = {0, 0, 0, 0};
-    for (uint32_t s0 = 0; s0 < slices; s0 += kAhead) {
+    for (uint32_t s0 = first; s0 < end; s0 += kAhead) {
         f32x4 v[kAhead];
 #pragma unroll
         for (uint32_t a = 0; a < kAhead; ++a) {
-            const float *p = part + min(s0 + a, slices - 1) * all + at;
+            const float *p = part + min(s0 + a, end - 1) * all;
             if (have == 4) {
                 typedef f32x4 any __attribute__((aligned(4)));
-                v[a] = *reinterpret_cast<const any *>(p);
+                v[a] = *reinterpret_cast<const any *>(p + i);
             } else {
 #pragma unroll
-                for (uint32_t j = 0; j < 4; ++j) v[a][j] = j < have ? p[j] : 0.0f;
+                for (uint32_t j = 0; j < 4; ++j) v[a][j] = j < have ? p[i + j] : 0.0f;
             }
         }
 #pragma unroll
         for (uint32_t a = 0; a < kAhead; ++a)
-            if (s0 + a < slices) sum += v[a];
+            if (s0 + a < end) sum += v[a];
     }
+    sums[share][lane] = sum;
+    __syncthreads();
+    if (share) return;
+#pragma unroll
+    for (uint32_t w = 1; w < kShares; ++w) sum += sums[w][lane];
 #pragma unroll
     for (uint32_t j = 0; j < 4; ++j) {
-        const uint64_t e = at + j;
-        if (j >= have || e < i) continue;  // an earlier lane's
-        T *p = out + e / k * ld_out + e % k;
+        if (j >= have) continue;
+        T *p = out + (i + j) / k * ld_out + (i + j) % k;
         *p = (T)(sum[j] + (add ? widen(*p) : 0.0f));
     }
 }
 
-// Tile sides: 256 (a wave's 128 x 128 part reads the least from LDS for each
-// product), or 128 where that leaves workgroup slots empty.
+// Tiles of 256 x 256 (a wave's 128 x 128 part reads the least from LDS for
+// each product) where there are enough of them for three quarters of the 256
+// CUs, else of 128 x 128, two workgroups to a CU.  Fewer of those than CUs
+// share t in slices of at least 8 LDS tiles: 512 x 512 of 8192 rows takes 19 us
+// so and 22 us in slices of 4, 512 x 512 of 512 rows 12 and 17 us.
 uint64_t tiles_of(uint64_t n, uint64_t k, uint32_t side) { return ((n + side - 1) / side) * ((k + side - 1) / side); }
 
 struct Plan {
@@ -541,7 +551,7 @@ Plan plan_of(uint64_t t, uint64_t n, uint64_t k) {
     p.side = tiles_of(n, k, 256) >= 192 ? 256 : 128;
     const uint64_t tiles = tiles_of(n, k, p.side);
     p.slices = 1;
-    if (p.side == 128 && tiles < 256 && steps >= 8) p.slices = (uint32_t)std::min<uint64_t>(512 / tiles, steps / 4);
+    if (p.side == 128 && tiles < 256 && steps >= 16) p.slices = (uint32_t)std::min<uint64_t>(512 / tiles, steps / 8);
     p.slice = (uint32_t)((steps + p.slices - 1) / p.slices);
     return p;
 }
@@ -584,7 +594,7 @@ hipError_t launch_q8_weight_grad(const void *dy, int dtype, uint64_t ld_dy, uint
     if (split)
         with_dtype(dw_dtype, [&](auto o) {
             constexpr int ODT = decltype(o)::value;
-            hipLaunchKernelGGL(join_kernel<ODT>, dim3((uint32_t)((n * k + 4 * kThreads - 1) / (4 * kThreads))), dim3(kThreads), 0,
+            hipLaunchKernelGGL(join_kernel<ODT>, dim3((uint32_t)((n * k + 4 * kWave - 1) / (4 * kWave))), dim3(kThreads), 0,
                                stream, static_cast<const float *>(ws), p.slices, n, k, ld_dw,
                                static_cast<typename Plain<ODT>::type *>(dw), (uint32_t)accumulate);
         });
