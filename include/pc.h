@@ -345,7 +345,7 @@ pc_status pc_traffic_probe(const void *d_src, void *d_dst, size_t bytes, void *s
  * for no number (0x7F and 0xFF in e4m3, 0x80 in int8) reads as NaN.  Powers
  * of two keep every stored value exact in bf16 and f32, so the matrix
  * instructions multiply stored values without rounding them again.  Scale
- * codes run from 1 to 254; pc_q8_store writes 10 to 248.
+ * codes run from 1 to 254; pc_q8_store writes 10 to 249.
  *
  * Tensors of plain numbers are f32, f16 or bf16, rows of unit stride and a
  * row distance `ld` in elements that may exceed the width; pointers need the
@@ -429,7 +429,8 @@ pc_status pc_q8_glu_backward(const void *d_dh, int dtype, size_t ld_dh, const pc
  * three times the operations).
  *   d_ws, ws_bytes  scratch of pc_q8_weight_grad_workspace_bytes (which may
  *             be 0, then d_ws may be NULL), 16-byte aligned.
- * x->rows == 0: dW = 0, or stays where accumulate.
+ * x->rows == 0: dW = 0, or stays where accumulate.  Row distances of dy and
+ * x of 2^24 elements and more: PC_ERR_UNSUPPORTED.
  */
 size_t pc_q8_weight_grad_workspace_bytes(size_t rows, size_t n_out, size_t n_in, int dy_dtype);
 pc_status pc_q8_weight_grad(const void *d_dy, int dy_dtype, size_t ld_dy, size_t n_out, const pc_q8 *x, void *d_dw,

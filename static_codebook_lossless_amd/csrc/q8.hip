@@ -5,7 +5,13 @@
 // All three read and write every byte once and compute little: they are
 // bound by HBM.  A lane handles 8 columns (16 bytes of a 16-bit type, 8
 // symbols), so four neighbouring lanes hold a group, and the largest
-// magnitude of a group costs two DPP exchanges and no LDS.
+// magnitude of a group costs two DPP exchanges and no LDS.  Tensors whose rows
+// lie end to end in whole groups count as one row and need no division.
+//
+// Measured at 4096 x 16384 bf16 (a device copy reaches 5.2 TB/s): store 33 us
+// (6.1 TB/s), with the histogram 49 us, load 30 us (6.8 TB/s), the backward
+// pass of gate and up in one tensor with h 115 us (5.9 TB/s).  Small calls
+// (32 x 2048) take 4.4 us on the device and 9 us on the host.
 #include <algorithm>
 #include <type_traits>
 
@@ -23,7 +29,12 @@ constexpr uint32_t kTile = kThreads * kPerLane;
 // ---------------------------------------------------------------------------
 
 // Histogram of the symbols in LDS, as in the byte histogram but with 8 copies
-// per wave, 257 words apart, added to the caller's counts at the end.
+// per wave, 257 words apart, added to the caller's counts at the end.  One
+// workgroup of 16 waves fills a CU: the sums at the end cost 15 ns for every
+// workgroup, as they meet at the same 256 addresses.  64 Mi bf16 elements:
+// two workgroups of 4 waves and 16 copies 89 us, four of 4 and 8 copies 67 us,
+// the same with the next tile's loads ahead 60 us, one of 16 waves 51 us (4
+// copies: 60 us).
 constexpr uint32_t kCopies = 8;
 constexpr uint32_t kCopyStride = 257;
 constexpr uint32_t kCountThreads = 1024;

@@ -6,6 +6,16 @@
 // there, as the scales are powers of two), and the transposing LDS reads hand
 // every lane the consecutive t of one column that the matrix instruction
 // takes.
+//
+// Bound by the matrix cores at their sustained clock (large tiles): 4096 rows,
+// 11008 x 4096 from e4m3 and bf16 into f32 take 322-343 us (1.08-1.15 PFLOP/s);
+// the matrix instructions alone, without loads and LDS, take 305 us, as 688
+// tiles are 2.7 rounds of 256 CUs.  A library product of the same shape with x
+// already in bf16 takes 379 us.  int8 takes 499 us: its symbols need 4.5 vector
+// instructions each, e4m3's half a one.  Small tiles with a long t (32768 rows,
+// 320 x 1000, int8) take 53 us and 7 us to join their slices; there the vector
+// work, the LDS and the matrix cores each take a third of the time and overlap
+// only between the two waves of a SIMD.
 #include <algorithm>
 #include <type_traits>
 
@@ -545,10 +555,10 @@ struct Plan {
     uint32_t side, slices, slice;
 };
 
-Plan plan_of(uint64_t t, uint64_t n, uint64_t k) {
+Plan plan_of(uint64_t t, uint64_t n, uint64_t k, int dtype) {
     Plan p;
     const uint64_t steps = (t + kStep - 1) / kStep;
-    p.side = tiles_of(n, k, 256) >= 192 ? 256 : 128;
+    p.side = dtype == PC_BF16 && tiles_of(n, k, 256) >= 192 ? 256 : 128;
     const uint64_t tiles = tiles_of(n, k, p.side);
     p.slices = 1;
     if (p.side == 128 && tiles < 256 && steps >= 16) p.slices = (uint32_t)std::min<uint64_t>(512 / tiles, steps / 8);
@@ -558,15 +568,15 @@ Plan plan_of(uint64_t t, uint64_t n, uint64_t k) {
 
 }  // namespace
 
-uint64_t wgrad_workspace(uint64_t t, uint64_t n, uint64_t k, int) {
-    const Plan p = plan_of(t, n, k);
+uint64_t wgrad_workspace(uint64_t t, uint64_t n, uint64_t k, int dtype) {
+    const Plan p = plan_of(t, n, k, dtype);
     return p.slices > 1 ? (uint64_t)p.slices * n * k * 4 : 0;
 }
 
 hipError_t launch_q8_weight_grad(const void *dy, int dtype, uint64_t ld_dy, uint64_t n_out, const pc_q8 *x, void *dw,
                                  int dw_dtype, uint64_t ld_dw, bool accumulate, void *ws, hipStream_t stream) {
     const uint64_t t = x->rows, n = n_out, k = x->cols;
-    const Plan p = plan_of(t, n, k);
+    const Plan p = plan_of(t, n, k, dtype);
     const bool split = p.slices > 1;
     const Shape s = {t, n, k, ld_dy, x->ld_sym, x->ld_scale, split ? k : ld_dw, p.slice,
                      (uint32_t)((n + p.side - 1) / p.side), (uint32_t)((k + p.side - 1) / p.side)};
@@ -581,8 +591,10 @@ hipError_t launch_q8_weight_grad(const void *dy, int dtype, uint64_t ld_dy, uint
         auto by_side = [&](auto f, auto r) {
             constexpr int FMT = decltype(f)::value;
             constexpr bool RAGGED = decltype(r)::value;
-            p.side == 256 ? launch(wgrad_kernel<DT, FMT, RAGGED, 2, 2, 4, 4, 1>)
-                          : launch(wgrad_kernel<DT, FMT, RAGGED, 2, 2, 2, 2, 2>);
+            if constexpr (DT == PC_BF16) {
+                if (p.side == 256) return launch(wgrad_kernel<DT, FMT, RAGGED, 2, 2, 4, 4, 1>);
+            }
+            launch(wgrad_kernel<DT, FMT, RAGGED, 2, 2, 2, 2, 2>);
         };
         auto by_format = [&](auto r) {
             if (x->format == PC_Q8_E4M3) by_side(std::integral_constant<int, PC_Q8_E4M3>(), r);

@@ -10,7 +10,7 @@ distance (``view(-1, cols)``).  Wrong types, sizes, strides or devices raise
 """
 from __future__ import annotations
 
-import ctypes as C
+import math
 
 import torch
 
@@ -48,7 +48,7 @@ def _rows(t, what):
         if t.dim() == 0:
             raise ValueError("%s must have a dimension" % what)
         try:
-            t = t.view(-1, t.shape[-1]) if t.numel() else t.new_empty(t[..., 0].numel(), t.shape[-1])
+            t = t.view(math.prod(t.shape[:-1]), t.shape[-1])
         except RuntimeError:
             raise ValueError("the leading dimensions of %s do not collapse into rows" % what) from None
     rows, cols = t.shape
@@ -104,13 +104,17 @@ class Q8:
             raise TypeError("symbols and scales must be uint8")
         if symbols.dim() != 2 or scales.dim() != 2:
             raise ValueError("symbols and scales must have two dimensions")
-        symbols, ld = _rows(symbols, "symbols")
-        scales, ld_scale = _rows(scales, "scales")
-        _same_device(symbols, scales, "scales")
         rows, cols = symbols.shape
-        if scales.shape != (rows, -(-cols // PC_Q8_GROUP)):
+        groups = -(-cols // PC_Q8_GROUP)
+        if scales.shape != (rows, groups):
             raise ValueError("scales must be [rows, ceil(cols / 32)] = [%d, %d], not %s"
-                             % (rows, -(-cols // PC_Q8_GROUP), list(scales.shape)))
+                             % (rows, groups, list(scales.shape)))
+        if symbols.is_cuda and symbols.is_contiguous() and scales.is_contiguous():
+            ld, ld_scale = cols, groups
+        else:
+            symbols, ld = _rows(symbols, "symbols")
+            scales, ld_scale = _rows(scales, "scales")
+        _same_device(symbols, scales, "scales")
         self.symbols, self.scales, self.format = symbols, scales, format
         self.arg = StoredArg(symbols.data_ptr(), scales.data_ptr(), rows, cols, ld, ld_scale, code, 0)
 
@@ -211,7 +215,8 @@ def pc_q8_glu_backward(dh, gate: Q8, up: Q8 | None = None, act="silu", with_h=Fa
     ``dh`` is [rows, cols].  Without ``up``, a ``gate`` of 2 * cols columns
     holds gate and up side by side (cols a multiple of 32), and one of cols
     columns is an activation without a gate, ``h = act(gate)``.  Gradients and
-    ``h`` have dh's dtype."""
+    ``h`` are [rows, cols] of dh's dtype (a dh of more dimensions counts as
+    rows of its last one)."""
     kind, a = _dtype(dh.dtype, "dh"), _code(_ACTS, act, "act")
     x, ld = _rows(dh, "dh")
     rows, cols = x.shape

@@ -178,6 +178,7 @@ def test_store_and_load_of_views():
 
 
 def test_nothing_to_store():
+    assert pc.pc_q8_store(torch.empty((2, 3, 0), device=DEV)).shape == (6, 0)
     for shape in ((0, 64), (5, 0), (0, 0)):
         q = pc.pc_q8_store(torch.empty(shape, device=DEV))
         assert q.symbols.shape == shape and pc.pc_q8_load(q).shape == shape
@@ -344,18 +345,24 @@ def test_weight_grad(dtype, fmt):
         check_wgrad(np64(dy), x, out, odt, np64(old))
 
 
-def test_weight_grad_of_many_tiles():
-    # more tiles than one round of workgroups, ragged on every side; products against 64-bit ones on the device
+@pytest.mark.parametrize("t,n,k,fmt", [(777, 4200, 3976, "e4m3"), (640, 4096, 3840, "e4m3"), (333, 4096, 3840, "int8"),
+                                       (200, 4099, 3845, "int8"), (70, 4099, 3845, "e4m3")])
+def test_weight_grad_of_many_tiles(t, n, k, fmt):
+    # the large tiles, whole and ragged on every side; products against 64-bit ones on the device
     g = torch.Generator(device=DEV).manual_seed(1)
-    t, n, k = 777, 4200, 4000 - 24
     x = torch.randn(t, k, generator=g, device=DEV)
     dy = torch.randn(t, n, generator=g, device=DEV).to(torch.bfloat16)
-    q = pc.pc_q8_store(x, "e4m3")
+    q = pc.pc_q8_store(x, fmt)
     v = pc.pc_q8_load(q, torch.float32).double()
-    got = pc.pc_q8_weight_grad(dy, q).double()
     want = torch.mm(dy.double().t().contiguous(), v)
     size = torch.mm(dy.double().abs().t().contiguous(), v.abs())
-    assert bool((torch.abs(got - want) <= (t + 3) * 2.0 ** -23 * size + 2.0 ** -24 * want.abs()).all())
+    got = pc.pc_q8_weight_grad(dy, q)
+    tol = (t + 3) * 2.0 ** -23 * size + 2.0 ** -24 * want.abs()
+    assert bool((torch.abs(got.double() - want) <= tol).all())
+    half = pc.pc_q8_weight_grad(dy, q, dtype=torch.bfloat16)
+    assert bool((torch.abs(half.double() - want) <= tol + 2.0 ** -8 * want.abs()).all())
+    pc.pc_q8_weight_grad(dy, q, out=got, accumulate=True)
+    assert bool((torch.abs(got.double() - 2 * want) <= 3 * tol).all())
 
 
 def test_weight_grad_of_views_and_nothing():
@@ -383,14 +390,15 @@ def test_weight_grad_of_views_and_nothing():
         pc.pc_q8_weight_grad(dy, q, accumulate=True)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
-def test_weight_grad_carries_infinity_and_nan(dtype):
+def test_weight_grad_carries_infinity_and_nan(dtype, fmt):
     rng = np.random.default_rng(13)
-    q, x = make_q8(rng, 40, 64, "e4m3")
+    q, x = make_q8(rng, 40, 64, fmt)
     dy = np.ones((40, 16), dtype=np.float32)
     dy[3, 2], dy[5, 4] = math.inf, math.nan
     sym = q.symbols.clone()
-    sym[7, 9] = 0x7F
+    sym[7, 9] = q8.NAN_BYTE[fmt]
     got = np64(pc.pc_q8_weight_grad(tensor(dy, dtype), q.with_symbols(sym)))
     v = x.copy()
     v[7, 9] = math.nan

@@ -104,6 +104,7 @@ def test_weight_grad_workspace():
     assert wgrad(n=0, dw=None) == OK
     assert wgrad(x=q8(rows=0), acc=1) == OK
     assert wgrad(n=1 << 31, ld=1 << 31) == BIG
+    assert wgrad(ld=1 << 24) == BIG and wgrad(x=q8(ld=1 << 24)) == BIG and wgrad(x=q8(lds=1 << 24)) == BIG
 
 
 @pytest.mark.parametrize("kw", [dict(tok=None), dict(tb=2), dict(tok=A + 4), dict(table=None), dict(dtype=9),
