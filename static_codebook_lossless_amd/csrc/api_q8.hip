@@ -160,9 +160,9 @@ pc_status pc_embed_backward(const void *d_dy, int dy_dtype, size_t ld_dy, const 
     if (n && (!plain_ok(d_dy, dy_dtype, dim, ld_dy) || !d_tokens ||
               (reinterpret_cast<uintptr_t>(d_tokens) & (token_bytes - 1))))
         return PC_ERR_INVALID_ARG;
-    // the sums take a wave for every 32 sorted tokens and 512 columns, the zeros one for every row
+    // the sums take at most a wave for every 8 sorted tokens and 512 columns, the zeros one for every row
     if (n >= kMaxWidth || vocab > kMaxWidth || !size_ok(n, dim) || !size_ok(vocab, dim) || !span_ok(vocab, ld_grad) ||
-        (n && !span_ok(n, ld_dy)) || (n + 31) / 32 * ((dim + 511) / 512) + vocab / 4 >= kMaxGroups || (dim + 511) / 512 > 65535)
+        (n && !span_ok(n, ld_dy)) || (n + 7) / 8 * ((dim + 511) / 512) + vocab / 4 >= kMaxGroups || (dim + 511) / 512 > 65535)
         return PC_ERR_UNSUPPORTED;
     const size_t need = pc_embed_backward_workspace_bytes(n, dim, vocab);
     if (need) {

@@ -2,8 +2,9 @@
 //
 // Both are bound by HBM.  Measured: 32768 rows of 4096 out of an int8 table of
 // 32000 into bf16 53 us (306 MB); the gradient of 32768 x 4096 bf16 to a table of
-// 32000 in f32, tokens by 1/rank, 190 us (793 MB): sort 27, sums and zeros 151,
-// join 11; of 511 x 1000 f32 to a table of 4001 9 us in one launch.
+// 32000 in f32, tokens by 1/rank, 192 us (793 MB): sort 29, sums and zeros 152,
+// join 12; of 2048 x 1000 bf16 to a table of 4001 17 us (7, 6 and 4 on the
+// device); of 511 x 1000 f32 9 us in one launch.
 #include <algorithm>
 #include <type_traits>
 
@@ -187,7 +188,7 @@ __device__ __forceinline__ void put_row(typename Plain<ODT>::type *row, const Co
 // order, with their places), and its waves sum the rows one by one; a row
 // with many tokens is summed by all waves, a share of its tokens each.  Rows
 // without tokens become zero in passing.
-constexpr uint32_t kSmall = 1024;        // tokens
+constexpr uint32_t kSmall = 512;         // tokens
 constexpr uint32_t kSmallThreads = 256;
 constexpr uint32_t kSmallWaves = kSmallThreads / kWave;
 constexpr uint32_t kMany = 32;           // tokens of a row that are shared among the waves
@@ -337,6 +338,7 @@ constexpr uint32_t kSortThreads = 1024;
 constexpr uint32_t kSortWaves = kSortThreads / kWave;
 constexpr uint32_t kMaxRange = 1000;  // tokens (rows of the table) of one workgroup: 16 counters each, in 64 KB of LDS
 constexpr uint32_t kTokensAhead = 8;
+constexpr int kMostLanes = 40;
 constexpr uint32_t kKept = 4;  // groups of 8 tokens that stay in a lane's registers
 constexpr uint32_t kResident = kSortThreads * kTokensAhead * kKept;
 
@@ -360,39 +362,66 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const void *__restri
     __syncthreads();
     uint32_t *my = cnt + wave * range;
     const uint32_t part = (n + kSortWaves * kWave - 1) / (kSortWaves * kWave) * kWave;
-    const uint32_t first = min(n, wave * part), last = min(n, first + part);
-    // tokens i0 + lane, i0 + 64 + lane, ..: their number in the range, -1 for
-    // one below it, -2 for any other
-    auto fetch = [&](uint32_t i0, int32_t r[kTokensAhead]) {
-        int64_t t[kTokensAhead];
+    const uint32_t first = uniform(min(n, wave * part)), last = uniform(min(n, first + part));
+    // tokens i0 + lane, i0 + 64 + lane, ..: their numbers in the range, ~0 for
+    // those outside it; `below` counts the tokens below the range, for the first pass
+    const uint32_t lo32 = (uint32_t)lo, most = (uint32_t)min(vocab, (uint64_t)1 << 31);
+    const uint32_t none = padding >= 0 && padding < (int64_t)most ? (uint32_t)padding : ~0u;
+    uint32_t below = 0;
+    auto fetch = [&](uint32_t i0, TOK t[kTokensAhead]) {
 #pragma unroll
         for (uint32_t k = 0; k < kTokensAhead; ++k) {
             const uint32_t i = i0 + k * kWave + lane;
-            t[k] = i < last ? token_at<TOK>(tokens, i) : -1;
-        }
-#pragma unroll
-        for (uint32_t k = 0; k < kTokensAhead; ++k) {
-            const bool ok = t[k] >= 0 && (uint64_t)t[k] < vocab && t[k] != padding;
-            r[k] = !ok ? -2 : (uint64_t)t[k] < lo ? -1 : (uint64_t)t[k] - lo < size ? (int32_t)(t[k] - lo) : -2;
+            t[k] = i < last ? static_cast<const TOK *>(tokens)[i] : (TOK)-1;
         }
     };
-    uint32_t below = 0;
-    int32_t kept[kKept][kTokensAhead];
-    auto count = [&](const int32_t r[kTokensAhead]) {
+    auto classify = [&](const TOK t[kTokensAhead], uint32_t r[kTokensAhead]) {
 #pragma unroll
         for (uint32_t k = 0; k < kTokensAhead; ++k) {
-            below += r[k] == -1;
-            if (r[k] >= 0) atomicAdd(&my[r[k]], 1u);
+            uint32_t key = (uint32_t)t[k];
+            if constexpr (sizeof(TOK) == 8) key = (uint64_t)t[k] >> 32 ? ~0u : key;
+            key = key < most && key != none ? key : ~0u;
+            below += key < lo32;
+            r[k] = key - lo32 < size ? key - lo32 : ~0u;
         }
     };
+    // Whether many lanes have one token and the others none: such lanes add up
+    // at once instead of one after the other at one counter (65536 tokens, nine
+    // in ten the same: 92 -> 39 us).
+    auto all_one = [&](uint32_t r, uint64_t mine, uint32_t &one) {
+        if (__popcll(mine) < kMostLanes) return false;
+        one = (uint32_t)__builtin_amdgcn_readlane((int)r, (int)__builtin_ctzll(mine));
+        return __ballot(r == one) == mine;
+    };
+    auto count = [&](const uint32_t r[kTokensAhead]) {
+#pragma unroll
+        for (uint32_t k = 0; k < kTokensAhead; ++k) {
+            const uint64_t mine = __ballot(r[k] != ~0u);
+            uint32_t one;
+            if (all_one(r[k], mine, one)) {
+                if (lane == 0) atomicAdd(&my[one], (uint32_t)__popcll(mine));
+            } else if (r[k] != ~0u) {
+                atomicAdd(&my[r[k]], 1u);
+            }
+        }
+    };
+    uint32_t kept[kKept][kTokensAhead];
+    constexpr uint32_t kGroupOfTokens = kTokensAhead * kWave;
     if constexpr (RESIDENT) {
+        TOK t[kKept][kTokensAhead];
 #pragma unroll
-        for (uint32_t g = 0; g < kKept; ++g) fetch(first + g * kTokensAhead * kWave, kept[g]);
+        for (uint32_t g = 0; g < kKept; ++g) fetch(first + g * kGroupOfTokens, t[g]);
 #pragma unroll
-        for (uint32_t g = 0; g < kKept; ++g) count(kept[g]);
+        for (uint32_t g = 0; g < kKept; ++g)
+            if (first + g * kGroupOfTokens < last) {
+                classify(t[g], kept[g]);
+                count(kept[g]);
+            }
     } else {
-        for (uint32_t i0 = first; i0 < last; i0 += kTokensAhead * kWave) {
-            fetch(i0, kept[0]);
+        for (uint32_t i0 = first; i0 < last; i0 += kGroupOfTokens) {
+            TOK t[kTokensAhead];
+            fetch(i0, t);
+            classify(t, kept[0]);
             count(kept[0]);
         }
     }
@@ -428,20 +457,22 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const void *__restri
     }
     if (tid == 0 && lo + size == vocab) out.start[vocab] = base;
     __syncthreads();
-    auto place = [&](const int32_t r[kTokensAhead], uint32_t i0) {
+    auto place = [&](const uint32_t r[kTokensAhead], uint32_t i0) {
 #pragma unroll
         for (uint32_t k = 0; k < kTokensAhead; ++k) {
-            const bool mine = r[k] >= 0;
+            const bool mine = r[k] != ~0u;
             uint64_t same = __ballot(mine);
             if (!same) continue;
-            for (uint32_t b = 0; b < bits; ++b) {
-                const uint64_t set = __ballot(r[k] >> b & 1);
-                same &= (r[k] >> b & 1) ? set : ~set;
-            }
+            uint32_t one;
+            if (!all_one(r[k], same, one))
+                for (uint32_t b = 0; b < bits; ++b) {
+                    const uint64_t set = __ballot(r[k] >> b & 1);
+                    same &= (r[k] >> b & 1) ? set : ~set;
+                }
             const uint32_t before = __popcll(same & ((1ull << lane) - 1));
             if (mine) {
                 const uint32_t at = my[r[k]] + before;
-                out.key[at] = (uint32_t)(lo + r[k]);
+                out.key[at] = lo32 + r[k];
                 out.source[at] = i0 + k * kWave + lane;
             }
             __builtin_amdgcn_wave_barrier();
@@ -451,10 +482,13 @@ __global__ __launch_bounds__(kSortThreads) void sort_kernel(const void *__restri
     };
     if constexpr (RESIDENT) {
 #pragma unroll
-        for (uint32_t g = 0; g < kKept; ++g) place(kept[g], first + g * kTokensAhead * kWave);
+        for (uint32_t g = 0; g < kKept; ++g)
+            if (first + g * kGroupOfTokens < last) place(kept[g], first + g * kGroupOfTokens);
     } else {
-        for (uint32_t i0 = first; i0 < last; i0 += kTokensAhead * kWave) {
-            fetch(i0, kept[0]);
+        for (uint32_t i0 = first; i0 < last; i0 += kGroupOfTokens) {
+            TOK t[kTokensAhead];
+            fetch(i0, t);
+            classify(t, kept[0]);
             place(kept[0], i0);
         }
     }
@@ -485,7 +519,7 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(const typename Plain<DT>:
     const uint32_t count = uniform(in.start[vocab]);
     const uint32_t p0 = b * block;
     if (p0 >= count) return;
-    const uint32_t places = min(block, count - p0);  // at most 32
+    const uint32_t places = min(block, count - p0);
     // lane i: the key of place p0 + i - 1 (lane 0 the place before the block, if any), the row of place p0 + i
     const bool has = lane <= places + 1 && p0 + lane >= 1 && p0 + lane - 1 < count;
     const uint32_t key = has ? in.key[p0 + lane - 1] : ~0u;
@@ -529,12 +563,15 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(const typename Plain<DT>:
 // Joins the partial sums of the run that starts in block b and crosses its
 // end, in the order of the blocks: each wave of the workgroup takes an equal
 // share of them, and wave 0 adds up the waves.
-template <int ODT, bool WHOLE>
-__global__ __launch_bounds__(kThreads) void join_kernel(Sorted in, uint64_t vocab, uint64_t dim, uint32_t block,
+// Most workgroups find no such run and end: where there are many, they are of
+// four waves, else of eight (8184 of eight waves: 26 us, of four 12; one run
+// over 2048 blocks: 69 us with four, 42 with eight).
+template <int ODT, bool WHOLE, uint32_t THREADS>
+__global__ __launch_bounds__(THREADS) void join_kernel(Sorted in, uint64_t vocab, uint64_t dim, uint32_t block,
                                                         uint32_t slabs, Target to,
                                                         typename Plain<ODT>::type *__restrict__ grad,
                                                         uint64_t ld_grad) {
-    __shared__ float part[kThreads / kWave][kUnit][kWave];
+    __shared__ float part[THREADS / kWave][kUnit][kWave];
     const uint32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
     const uint32_t b = blockIdx.x / slabs, p1 = (b + 1) * block;  // below the number of tokens
     const Columns<WHOLE> cols(blockIdx.x % slabs, lane, dim);
@@ -543,7 +580,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(Sorted in, uint64_t voca
     const uint32_t begin = uniform(in.start[key]), end = uniform(in.start[key + 1]);
     if (begin < b * block) return;
     const uint32_t last = (end - 1) / block;  // the run's parts: block b's second, then the first of b + 1 .. last
-    const uint32_t each = (last - b + 1 + kThreads / kWave - 1) / (kThreads / kWave);
+    const uint32_t each = (last - b + 1 + THREADS / kWave - 1) / (THREADS / kWave);
     const uint32_t from = b + wave * each, till = min(last + 1, from + each);
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     for (uint32_t i0 = from; i0 < till; i0 += kAhead) {
@@ -566,11 +603,24 @@ __global__ __launch_bounds__(kThreads) void join_kernel(Sorted in, uint64_t voca
     if (wave) return;
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-        for (uint32_t w = 1; w < kThreads / kWave; ++w) acc[k] += part[w][k][lane];
+        for (uint32_t w = 1; w < THREADS / kWave; ++w) acc[k] += part[w][k][lane];
     put_row<ODT>(grad + (uint64_t)key * ld_grad, cols, acc, to);
 }
 
-constexpr uint32_t kBlock = 32;  // sorted places summed by one wave (two lanes are left for its neighbours)
+// Sorted places that one wave sums, at most 62 (a lane each, and two for the
+// neighbours): 32, or 8, whose loads are all in flight at once, where that
+// still leaves fewer than four waves to a SIMD.
+uint32_t block_of(uint64_t n, uint64_t slabs) { return n * slabs <= 32768 ? 8 : 32; }
+uint64_t slabs_of(uint64_t dim) { return (dim + kSlab - 1) / kSlab; }
+
+// One launch or three: the one pays for few tokens of a small range each.
+// 4001 x 1000, 512 tokens: 9 us against 22; 32000 x 2048 (62 rows a
+// workgroup), 512 tokens by 1/rank: 82 us against 62.
+constexpr uint64_t kSmallRange = 16;
+uint64_t small_range(uint64_t vocab, uint64_t slabs) { return std::max<uint64_t>(4, vocab * slabs / 2048); }
+bool is_small(uint64_t n, uint64_t vocab, uint64_t dim) {
+    return n <= kSmall && small_range(vocab, slabs_of(dim)) <= kSmallRange;
+}
 
 uint32_t range_of(uint64_t vocab) {
     const uint64_t r = std::max<uint64_t>(64, (vocab + 255) / 256);
@@ -582,8 +632,8 @@ uint64_t up16(uint64_t b) { return (b + 15) / 16 * 16; }
 }  // namespace
 
 uint64_t embed_backward_workspace(uint64_t n, uint64_t dim, uint64_t vocab) {
-    if (n <= kSmall) return 0;
-    const uint64_t blocks = (n + kBlock - 1) / kBlock;
+    if (is_small(n, vocab, dim)) return 0;
+    const uint64_t block = block_of(n, slabs_of(dim)), blocks = (n + block - 1) / block;
     return up16((vocab + 1) * 4) + 2 * up16(n * 4) + up16(blocks * 2 * dim * 4);
 }
 
@@ -616,12 +666,12 @@ hipError_t launch_embed(const void *tokens, int token_bytes, uint64_t n, const v
 hipError_t launch_embed_backward(const void *dy, int dtype, uint64_t ld_dy, const void *tokens, int token_bytes,
                                  uint32_t n, uint64_t dim, uint64_t vocab, int64_t padding, float scale, void *grad,
                                  int grad_dtype, uint64_t ld_grad, bool accumulate, void *ws, hipStream_t stream) {
-    const uint32_t slabs = (uint32_t)((dim + kSlab - 1) / kSlab);
+    const uint32_t slabs = (uint32_t)slabs_of(dim);
     const Target to = {scale, accumulate};
     const bool whole = dim % 4 == 0;
-    if (n <= kSmall) {
+    if (is_small(n, vocab, dim)) {
         // about 2048 workgroups, of at least 4 rows: each reads all tokens
-        const uint64_t each = std::min<uint64_t>(1u << 20, std::max<uint64_t>(4, vocab * slabs / 2048));
+        const uint64_t each = small_range(vocab, slabs);
         const dim3 grid((uint32_t)((vocab + each - 1) / each), slabs);
         with_dtype(grad_dtype, [&](auto o) {
             constexpr int ODT = decltype(o)::value;
@@ -643,7 +693,7 @@ hipError_t launch_embed_backward(const void *dy, int dtype, uint64_t ld_dy, cons
         });
         return hipGetLastError();
     }
-    const uint32_t range = range_of(vocab), blocks = (n + kBlock - 1) / kBlock;
+    const uint32_t range = range_of(vocab), block = block_of(n, slabs), blocks = (n + block - 1) / block;
     uint32_t bits = 0;
     while ((1u << bits) < range) ++bits;
     uint8_t *p = static_cast<uint8_t *>(ws);
@@ -670,12 +720,18 @@ hipError_t launch_embed_backward(const void *dy, int dtype, uint64_t ld_dy, cons
         typedef typename Plain<ODT>::type T;
         with_dtype(dtype, [&](auto d) {
             constexpr int DT = decltype(d)::value;
+            if (grid.x == 0) return;
             hipLaunchKernelGGL((sum_kernel<DT, ODT, WHOLE>), grid, dim3(kThreads), 0, stream,
-                               static_cast<const typename Plain<DT>::type *>(dy), ld_dy, s, vocab, dim, kBlock, blocks,
+                               static_cast<const typename Plain<DT>::type *>(dy), ld_dy, s, vocab, dim, block, blocks,
                                slabs, to, static_cast<T *>(grad), ld_grad);
         });
-        hipLaunchKernelGGL((join_kernel<ODT, WHOLE>), dim3((blocks - 1) * slabs), dim3(kThreads), 0, stream, s, vocab,
-                           dim, kBlock, slabs, to, static_cast<T *>(grad), ld_grad);
+        const uint32_t joins = blocks > 1 ? (blocks - 1) * slabs : 0;
+        auto join = [&](auto k, uint32_t threads) {
+            hipLaunchKernelGGL(k, dim3(joins), dim3(threads), 0, stream, s, vocab, dim, block, slabs, to,
+                               static_cast<T *>(grad), ld_grad);
+        };
+        if (joins > 4096) join(join_kernel<ODT, WHOLE, 256>, 256);
+        else if (joins) join(join_kernel<ODT, WHOLE, 512>, 512);
     };
     with_dtype(grad_dtype, [&](auto o) {
         if (whole) sums(o, std::true_type());
