@@ -182,8 +182,7 @@ __device__ __forceinline__ void put_row(typename Plain<ODT>::type *row, const Co
     store_columns<ODT, true>(row, c, s);
 }
 
-// Few tokens: one launch (the three below took 41 us for 511 tokens, most of
-// it waiting for one dependent load after the other).  A workgroup owns a range of the table's rows and a
+// Few tokens: one launch.  A workgroup owns a range of the table's rows and a
 // slab of columns.  It reads all tokens, keeps those of its range in LDS (in
 // order, with their places), and its waves sum the rows one by one; a row
 // with many tokens is summed by all waves, a share of its tokens each.  Rows
@@ -614,8 +613,8 @@ uint32_t block_of(uint64_t n, uint64_t slabs) { return n * slabs <= 32768 ? 8 : 
 uint64_t slabs_of(uint64_t dim) { return (dim + kSlab - 1) / kSlab; }
 
 // One launch or three: the one pays for few tokens of a small range each.
-// 4001 x 1000, 512 tokens: 9 us against 22; 32000 x 2048 (62 rows a
-// workgroup), 512 tokens by 1/rank: 82 us against 62.
+// 4001 x 1000, 512 tokens: 9 us against 16; 32000 x 2048 (62 rows a
+// workgroup), 512 tokens by 1/rank: 82 us against 57.
 constexpr uint64_t kSmallRange = 16;
 uint64_t small_range(uint64_t vocab, uint64_t slabs) { return std::max<uint64_t>(4, vocab * slabs / 2048); }
 bool is_small(uint64_t n, uint64_t vocab, uint64_t dim) {

@@ -13,10 +13,8 @@ constexpr uint32_t kUnit = 8;             // columns one lane handles at a time
 constexpr uint32_t kUnitsPerGroup = kGroup / kUnit;
 constexpr uint32_t kMinCode = 10;         // 2^-117: the smallest element (2^-9 in e4m3) stays a normal number
 
-typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
@@ -244,7 +242,5 @@ __host__ __device__ inline bool with_dtype(int dtype, F &&f) {
     }
     return false;
 }
-
-inline size_t dtype_size(int dtype) { return dtype == PC_F32 ? 4 : 2; }
 
 }  // namespace pc

@@ -8,12 +8,12 @@
 // takes.
 //
 // Bound by the matrix cores at their sustained clock (large tiles): 4096 rows,
-// 11008 x 4096 from e4m3 and bf16 into f32 take 322-343 us (1.08-1.15 PFLOP/s);
+// 11008 x 4096 from e4m3 and bf16 into f32 take 317-343 us (1.08-1.17 PFLOP/s);
 // the matrix instructions alone, without loads and LDS, take 305 us, as 688
 // tiles are 2.7 rounds of 256 CUs.  A library product of the same shape with x
-// already in bf16 takes 379 us.  int8 takes 499 us: its symbols need 4.5 vector
+// already in bf16 takes 379 us.  int8 takes 494 us: its symbols need 4.5 vector
 // instructions each, e4m3's half a one.  Small tiles with a long t (32768 rows,
-// 320 x 1000, int8) take 53 us and 7 us to join their slices; there the vector
+// 320 x 1000, int8) take 51 us and 6 us to join their slices; there the vector
 // work, the LDS and the matrix cores each take a third of the time and overlap
 // only between the two waves of a SIMD.
 #include <algorithm>
@@ -245,8 +245,7 @@ __device__ __forceinline__ void interleave_three() {
     }
 }
 
-// SETS: tiles on their way in registers.
-template <int DT, int FMT, bool RAGGED, uint32_t WN, uint32_t WK, uint32_t FN, uint32_t FK, uint32_t SETS>
+template <int DT, int FMT, bool RAGGED, uint32_t WN, uint32_t WK, uint32_t FN, uint32_t FK>
 __global__ __launch_bounds__(WN *WK *kWave, FN * FK == 16 ? 1 : 2) void wgrad_kernel(const typename Plain<DT>::type *__restrict__ dy,
                                                                  const uint8_t *__restrict__ sym,
                                                                  const uint8_t *__restrict__ scale, Shape s,
@@ -270,8 +269,8 @@ __global__ __launch_bounds__(WN *WK *kWave, FN * FK == 16 ? 1 : 2) void wgrad_ke
     const uint32_t yc = tid % UN, yt = tid / UN, xc = tid % (UK / 2), xt = tid / (UK / 2);  // first pieces
     const uint32_t y_row = (uint32_t)s.ld_dy * kElem, x_row = (uint32_t)s.ld_sym, c_row = (uint32_t)s.ld_scale;
     const uint32_t y_at = yt * y_row + yc * 8 * kElem, x_at = xt * x_row + xc * 16, c_at = xt * c_row + xc / 2;
-    RawDy<DT, PY> ry[SETS];
-    RawX<FMT, PX> rx[SETS];
+    RawDy<DT, PY> ry;
+    RawX<FMT, PX> rx;
 
     // The operands from this slice's first row on.  Loads run ahead of the
     // products, past the slice's end, within the tensor; what they bring from
@@ -282,26 +281,26 @@ __global__ __launch_bounds__(WN *WK *kWave, FN * FK == 16 ? 1 : 2) void wgrad_ke
     const Window x0(sym + k0, x_row, t_first * x_row, rows, s.k - k0);
     const Window q0(scale + c0, c_row, t_first * c_row, rows, (s.k + kGroup - 1) / kGroup - c0);
     Window yw = y0, xw = x0, qw = q0;
-    auto load_dy = [&](RawDy<DT, PY> &r) {
-        r.load(yw.buffer(), y_at, RY * y_row);
+    auto load_dy = [&]() {
+        ry.load(yw.buffer(), y_at, RY * y_row);
         yw.down();
     };
-    auto load_x = [&](RawX<FMT, PX> &r) {
-        r.load(xw.buffer(), x_at, RX * x_row, qw.buffer(), c_at, RX * c_row);
+    auto load_x = [&]() {
+        rx.load(xw.buffer(), x_at, RX * x_row, qw.buffer(), c_at, RX * c_row);
         xw.down();
         qw.down();
     };
-    auto put_dy = [&](const RawDy<DT, PY> &r, auto which, uint32_t buf) {
+    auto put_dy = [&](auto which, uint32_t buf) {
         u32x4 *to = ly[buf] + yt * UN + swizzled(yc, yt);
 #pragma unroll
-        for (uint32_t p = 0; p < PY; ++p) to[p * RY * UN] = r.template piece<decltype(which)::value>(p);
+        for (uint32_t p = 0; p < PY; ++p) to[p * RY * UN] = ry.template piece<decltype(which)::value>(p);
     };
-    auto put_x = [&](const RawX<FMT, PX> &r, uint32_t buf) {
+    auto put_x = [&](uint32_t buf) {
         u32x4 *to = lx[buf] + xt * UK + swizzled(2 * xc, xt);
 #pragma unroll
         for (uint32_t p = 0; p < PX; ++p)
 #pragma unroll
-            for (uint32_t h = 0; h < 2; ++h) to[p * RX * UK + h] = r.piece(p, h);
+            for (uint32_t h = 0; h < 2; ++h) to[p * RX * UK + h] = rx.piece(p, h);
     };
     f32x16 acc[FN][FK];
 #pragma unroll
@@ -336,25 +335,26 @@ __global__ __launch_bounds__(WN *WK *kWave, FN * FK == 16 ? 1 : 2) void wgrad_ke
                 for (uint32_t j = 0; j < FK; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[which][i], fb[which][j], acc[i][j], 0, 0, 0);
         };
-        // Multiplies tile i out of its LDS buffer, puts tile i + 1 (register set
-        // R) into the other one and loads tile i + 1 + SETS.  The barrier stands
-        // before the last quarter of the products: by then the other waves'
-        // pieces of tile i + 1 are in LDS, and its first fragments arrive behind
-        // those products.
-        auto step = [&](auto set, auto which, uint32_t i) {
-            constexpr uint32_t R = decltype(set)::value, M = FN * FK;
+        // Multiplies tile i out of its LDS buffer, puts tile i + 1 into the other
+        // one and loads tile i + 2 (a second tile on its way in registers gained
+        // nothing: 55 against 52 us for 320 x 1000 of 32768 rows).  The barrier
+        // stands before the last quarter of the products: by then the other
+        // waves' pieces of tile i + 1 are in LDS, and its first fragments arrive
+        // behind those products.
+        auto step = [&](auto which, uint32_t i) {
+            constexpr uint32_t M = FN * FK;
             constexpr bool kFewVector = FMT == PC_Q8_E4M3 && kTerms<DT> == 1;
             const uint32_t buf = i & 1;
             read(1, buf, 1);
-            put_dy(ry[R], which, buf ^ 1);
+            put_dy(which, buf ^ 1);
             multiply(0);
             if (kFewVector) interleave<M, 0, 8, 0>();
-            load_dy(ry[R]);
+            load_dy();
             read(0, buf, 2);
-            put_x(rx[R], buf ^ 1);
+            put_x(buf ^ 1);
             multiply(1);
             if (kFewVector) interleave<M, 32, 8, 8, true>();
-            load_x(rx[R]);
+            load_x();
             read(1, buf, 3);
             multiply(0);
             if (kFewVector) interleave<M, 0, 0, 8>();
@@ -363,12 +363,6 @@ __global__ __launch_bounds__(WN *WK *kWave, FN * FK == 16 ? 1 : 2) void wgrad_ke
             read(0, buf ^ 1, 0);
             multiply(1);
             interleave<M, 0, 0, 0>();
-        };
-        auto run = [&](auto self, auto set, auto which, uint32_t i, uint32_t end) {
-            constexpr uint32_t R = decltype(set)::value;
-            if (R && i >= end) return;
-            step(std::integral_constant<uint32_t, (R + 1) % SETS>(), which, i);
-            if constexpr (R + 1 < SETS) self(self, std::integral_constant<uint32_t, R + 1>(), which, i + 1, end);
         };
         // Widths that are no multiple of a piece: a piece that sticks out of the
         // tensor's last row may lose the elements that are inside, as its load
@@ -383,23 +377,16 @@ __global__ __launch_bounds__(WN *WK *kWave, FN * FK == 16 ? 1 : 2) void wgrad_ke
             xw = x0;
             qw = q0;
             if (!RAGGED || whole) {
-                // tile 0 goes to LDS, tiles 1 .. SETS to the sets 1, .., SETS - 1, 0
-                load_dy(ry[0]);
-                load_x(rx[0]);
-#pragma unroll
-                for (uint32_t r = 1; r < SETS; ++r) {
-                    load_dy(ry[r]);
-                    load_x(rx[r]);
-                }
-                put_dy(ry[0], which, 0);
-                put_x(rx[0], 0);
-                load_dy(ry[0]);
-                load_x(rx[0]);
+                load_dy();
+                load_x();
+                put_dy(which, 0);
+                put_x(0);
+                load_dy();
+                load_x();
                 lds_barrier();
                 read(0, 0, 0);
 #pragma unroll 1
-                for (uint32_t i = 0; i < whole; i += SETS)
-                    run(run, std::integral_constant<uint32_t, 0>(), which, i, whole);
+                for (uint32_t i = 0; i < whole; ++i) step(which, i);
             }
             if constexpr (RAGGED) {
 #pragma unroll 1
@@ -411,15 +398,15 @@ __global__ __launch_bounds__(WN *WK *kWave, FN * FK == 16 ? 1 : 2) void wgrad_ke
                     xw.down(i);
                     qw.down(i);
                     const Window ye = yw, xe = xw;
-                    load_dy(ry[0]);
-                    load_x(rx[0]);
+                    load_dy();
+                    load_x();
                     const uint64_t cy = n0 + yc * 8, cx = k0 + xc * 16;
                     if (cy < s.n && cy + 8 > s.n) {
 #pragma unroll
                         for (uint32_t p = 0; p < PY; ++p) {
                             const uint32_t at = y_at + p * RY * y_row;
                             if (at < ye.left && at + 8 * kElem > ye.left)
-                                ry[0].load_single(p, ye.buffer(), at, (uint32_t)(s.n - cy));
+                                ry.load_single(p, ye.buffer(), at, (uint32_t)(s.n - cy));
                         }
                     }
                     if (cx < s.k && cx + 16 > s.k) {
@@ -427,12 +414,12 @@ __global__ __launch_bounds__(WN *WK *kWave, FN * FK == 16 ? 1 : 2) void wgrad_ke
                         for (uint32_t p = 0; p < PX; ++p) {
                             const uint32_t at = x_at + p * RX * x_row;
                             if (at < xe.left && at + 16 > xe.left)
-                                rx[0].load_single(p, xe.buffer(), at, (uint32_t)(s.k - cx));
+                                rx.load_single(p, xe.buffer(), at, (uint32_t)(s.k - cx));
                         }
                     }
                     lds_barrier();  // the other waves' reads of the last tile
-                    put_dy(ry[0], which, 0);
-                    put_x(rx[0], 0);
+                    put_dy(which, 0);
+                    put_x(0);
                     lds_barrier();
 #pragma unroll
                     for (uint32_t kk = 0; kk < kStep / 16; ++kk) {
@@ -545,10 +532,13 @@ __global__ __launch_bounds__(kThreads) void join_kernel(const float *__restrict_
 }
 
 // Tiles of 256 x 256 (a wave's 128 x 128 part reads the least from LDS for
-// each product) where there are enough of them for three quarters of the 256
-// CUs, else of 128 x 128, two workgroups to a CU.  Fewer of those than CUs
-// share t in slices of at least 8 LDS tiles: 512 x 512 of 8192 rows takes 19 us
-// so and 22 us in slices of 4, 512 x 512 of 512 rows 12 and 17 us.
+// each product) where there are enough of them for most of the 256 CUs, else of
+// 128 x 128, two workgroups to a CU: 2048 rows to 4096 x 4096 take 65 us in
+// large tiles and 81 in small ones, to 4096 x 2816 (176 large tiles) 54 and 59,
+// to 2048 x 4096 (128 large tiles) 51 and 41.  Fewer small tiles than CUs share
+// t in slices of at least 8 LDS tiles: 512 x 512 of 8192 rows takes 18 us so
+// and 22 us in slices of 4, 512 x 512 of 512 rows 12 and 17 us.  f16 and f32
+// gradients, of twice and three times the products, keep to the small tiles.
 uint64_t tiles_of(uint64_t n, uint64_t k, uint32_t side) { return ((n + side - 1) / side) * ((k + side - 1) / side); }
 
 struct Plan {
@@ -558,7 +548,7 @@ struct Plan {
 Plan plan_of(uint64_t t, uint64_t n, uint64_t k, int dtype) {
     Plan p;
     const uint64_t steps = (t + kStep - 1) / kStep;
-    p.side = dtype == PC_BF16 && tiles_of(n, k, 256) >= 192 ? 256 : 128;
+    p.side = dtype == PC_BF16 && tiles_of(n, k, 256) >= 160 ? 256 : 128;
     const uint64_t tiles = tiles_of(n, k, p.side);
     p.slices = 1;
     if (p.side == 128 && tiles < 256 && steps >= 16) p.slices = (uint32_t)std::min<uint64_t>(512 / tiles, steps / 8);
@@ -592,9 +582,9 @@ hipError_t launch_q8_weight_grad(const void *dy, int dtype, uint64_t ld_dy, uint
             constexpr int FMT = decltype(f)::value;
             constexpr bool RAGGED = decltype(r)::value;
             if constexpr (DT == PC_BF16) {
-                if (p.side == 256) return launch(wgrad_kernel<DT, FMT, RAGGED, 2, 2, 4, 4, 1>);
+                if (p.side == 256) return launch(wgrad_kernel<DT, FMT, RAGGED, 2, 2, 4, 4>);
             }
-            launch(wgrad_kernel<DT, FMT, RAGGED, 2, 2, 2, 2, 2>);
+            launch(wgrad_kernel<DT, FMT, RAGGED, 2, 2, 2, 2>);
         };
         auto by_format = [&](auto r) {
             if (x->format == PC_Q8_E4M3) by_side(std::integral_constant<int, PC_Q8_E4M3>(), r);
