@@ -196,17 +196,23 @@ __global__ __launch_bounds__(COUNT ? kCountThreads : kThreads) void store_kernel
 // load
 // ---------------------------------------------------------------------------
 
+// Two units a lane: four leave a small tensor too few workgroups (1021 x 5001
+// in f32: 9.0 us, with two 8.4), one costs large ones a little (64 Mi in bf16:
+// 30.3 us, with two 29.4).
+constexpr uint32_t kLoadPerLane = 2;
+constexpr uint32_t kLoadTile = kThreads * kLoadPerLane;
+
 template <int DT, int FMT>
 __global__ __launch_bounds__(kThreads) void load_kernel(const uint8_t *__restrict__ sym,
                                                         const uint8_t *__restrict__ scale, uint64_t ld_sym,
                                                         uint64_t ld_scale, Units units, uint64_t ld_out,
                                                         typename Plain<DT>::type *__restrict__ out) {
-    const uint64_t base = (uint64_t)blockIdx.x * kTile;
-    u32x2 w[kPerLane];
-    uint32_t code[kPerLane], n[kPerLane];
-    uint64_t row[kPerLane], col[kPerLane];
+    const uint64_t base = (uint64_t)blockIdx.x * kLoadTile;
+    u32x2 w[kLoadPerLane];
+    uint32_t code[kLoadPerLane], n[kLoadPerLane];
+    uint64_t row[kLoadPerLane], col[kLoadPerLane];
 #pragma unroll
-    for (uint32_t j = 0; j < kPerLane; ++j) {
+    for (uint32_t j = 0; j < kLoadPerLane; ++j) {
         const uint32_t local = j * kThreads + threadIdx.x;
         n[j] = 0;
         if (base + local < units.total) {
@@ -219,7 +225,7 @@ __global__ __launch_bounds__(kThreads) void load_kernel(const uint8_t *__restric
         }
     }
 #pragma unroll
-    for (uint32_t j = 0; j < kPerLane; ++j) {
+    for (uint32_t j = 0; j < kLoadPerLane; ++j) {
         if (!n[j]) continue;
         float v[8];
         unit_values<FMT>(w[j], scale_of(code[j]), v);
@@ -381,7 +387,7 @@ hipError_t launch_q8_store(const void *x, int dtype, uint64_t rows, uint64_t col
 
 hipError_t launch_q8_load(const pc_q8 *q, void *out, int dtype, uint64_t ld_out, hipStream_t stream) {
     const Units units = make_units(q->rows, q->cols, dense(q) && ld_out == q->cols);
-    const dim3 grid((uint32_t)((units.total + kTile - 1) / kTile));
+    const dim3 grid((uint32_t)((units.total + kLoadTile - 1) / kLoadTile));
     with_dtype(dtype, [&](auto d) {
         constexpr int DT = decltype(d)::value;
         auto launch = [&](auto k) {
