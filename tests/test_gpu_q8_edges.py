@@ -1,0 +1,42 @@
+"""Edges of the stored-tensor and embedding operators on the GPU: the ends of
+their number ranges, against 64-bit forms.  Tolerances were fixed before the
+first run and are derived where they are used.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import q8
+from test_gpu_q8 import DEV, _need_gpu, np64  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import static_codebook_lossless_amd as pc
+
+
+# -- activation backward -------------------------------------------------------------
+
+def test_gelu_keeps_its_digits_in_the_tail():
+    # y = g P(g) of g below zero is all tail.  In steps of 2^-24 (half a unit
+    # of 32 bits) its relative error is at most: b^2 / 2 times 2 of the
+    # exponent's factor and its rounding, 2 of the exponential, 2 of the reciprocal times the
+    # tail's slope in it (at most 8 over this range), 2 * 10 of ten
+    # multiply-adds times their condition (below 2), 6 of the products around
+    # them and the output's rounding
+    g = -np.concatenate([np.arange(1, 128) / 128.0, np.arange(64, 128) / 64.0 * 2.0, np.arange(64, 128) / 64.0 * 4.0])
+    rows = [np.pad(g[i:i + 32], (0, max(0, 32 - len(g[i:i + 32]))), mode="edge") for i in range(0, len(g), 32)]
+    sym, codes = q8.store(np.array(rows), "int8")
+    q = pc.Q8(torch.from_numpy(sym).to(DEV), torch.from_numpy(codes).to(DEV), "int8")
+    v = q8.load(sym, codes, "int8")
+    r = pc.pc_q8_glu_backward(torch.ones(v.shape, device=DEV), q, act="gelu", with_h=True)
+    tail = np.vectorize(lambda x: 0.5 * math.erfc(x / math.sqrt(2.0)))(-v)
+    want = v * tail
+    tol = (v * v + 2 + 16 + 40 + 6) * 2.0 ** -24
+    off = np.abs(np64(r.h) - want) / np.maximum(np.abs(want), 1e-300)
+    assert np.all(np.where(want == 0, np64(r.h) == 0, off <= tol)), float((off / tol).max())
+    # the slope is the difference of the tail and the density's product: the same, of either's size
+    density = v * np.exp(-v * v / 2) / math.sqrt(2 * math.pi)
+    assert np.all(np.abs(np64(r.gate) - (tail + density)) <= tol * (tail + np.abs(density)))
