@@ -39,7 +39,7 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(const void *__restrict_
     uint64_t row[kPerLane], col[kPerLane];
     uint32_t n[kPerLane];
     int64_t tok[kPerLane];
-    float v[kPerLane][8];
+    float v[kPerLane][8], by[kPerLane];
 #pragma unroll
     for (uint32_t j = 0; j < kPerLane; ++j) {
         const uint32_t local = j * kThreads + threadIdx.x;
@@ -53,7 +53,9 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(const void *__restrict_
 #pragma unroll
     for (uint32_t j = 0; j < kPerLane; ++j) {
         if (!n[j]) continue;
+        by[j] = scale;
         if (tok[j] < 0 || (uint64_t)tok[j] >= vocab) {
+            by[j] = 1.0f;  // zeros whatever the scale
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
             if (status && col[j] == 0) *status = PC_ERR_INVALID_ARG;
@@ -70,7 +72,7 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(const void *__restrict_
     for (uint32_t j = 0; j < kPerLane; ++j) {
         if (!n[j]) continue;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] *= scale;
+        for (int i = 0; i < 8; ++i) v[j][i] *= by[j];
         store_unit<ODT>(out + row[j] * ld_out + col[j], n[j], v[j]);
     }
 }

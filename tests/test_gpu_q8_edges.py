@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from oracle import q8
-from test_gpu_q8 import DEV, _need_gpu, np64  # noqa: F401
+from test_gpu_q8 import DEV, _need_gpu, activation, make_q8, np64  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +40,16 @@ def test_gelu_keeps_its_digits_in_the_tail():
     # the slope is the difference of the tail and the density's product: the same, of either's size
     density = v * np.exp(-v * v / 2) / math.sqrt(2 * math.pi)
     assert np.all(np.abs(np64(r.gate) - (tail + density)) <= tol * (tail + np.abs(density)))
+
+
+# -- embedding -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("scale", [math.inf, -math.inf, math.nan, -2.0])
+@pytest.mark.parametrize("table", ["f32", "bf16", "e4m3", "int8"])
+def test_rows_outside_the_table_are_zero_for_every_scale(table, scale):
+    rng = np.random.default_rng(35)
+    tab = make_q8(rng, 9, 50, table)[0] if table in q8.MOST else activation(rng, 9, 50, table)
+    tokens = torch.tensor([-1, 9, 1 << 35, 3], device=DEV)
+    out = pc.pc_embed(tokens, tab, scale=scale, dtype=torch.float32)
+    assert torch.all(out[:3] == 0)
+    assert not torch.all(out[3] == 0)
