@@ -307,7 +307,8 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(const void *__rest
         const uint32_t c = tokens_of(r);
         if (c > kMany || (c == 0 && to.add)) continue;
         sum(r, 0, 1, acc);
-        put_row<ODT>(grad + (lo + r) * ld_grad, cols, acc, to);
+        // a row without a token is zero whatever the scale
+        put_row<ODT>(grad + (lo + r) * ld_grad, cols, acc, Target{c ? to.scale : 1.0f, to.add});
     }
     if (count <= kMany) return;
     for (uint32_t q = 0; q < many; ++q) {

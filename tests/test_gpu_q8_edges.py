@@ -53,3 +53,17 @@ def test_rows_outside_the_table_are_zero_for_every_scale(table, scale):
     out = pc.pc_embed(tokens, tab, scale=scale, dtype=torch.float32)
     assert torch.all(out[:3] == 0)
     assert not torch.all(out[3] == 0)
+
+
+@pytest.mark.parametrize("scale", [math.inf, -math.inf, math.nan, -2.0])
+@pytest.mark.parametrize("n,vocab,dim", [(20, 300, 40), (300, 100, 33), (5000, 300, 40)])
+def test_rows_without_a_token_are_zero_for_every_scale(n, vocab, dim, scale):
+    rng = np.random.default_rng(36)
+    tokens = rng.integers(0, vocab // 2, n)
+    dy = activation(rng, n, dim, "f32")
+    got = pc.pc_embed_backward(dy, torch.from_numpy(tokens).to(DEV), vocab, scale=scale)
+    none = np.bincount(tokens, minlength=vocab) == 0
+    assert torch.all(got[torch.from_numpy(none).to(DEV)] == 0)
+    old = torch.full((vocab, dim), 4.0, device=DEV)
+    pc.pc_embed_backward(dy, torch.from_numpy(tokens).to(DEV), vocab, scale=scale, out=old, accumulate=True)
+    assert torch.all(old[torch.from_numpy(none).to(DEV)] == 4.0)
