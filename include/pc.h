@@ -464,7 +464,11 @@ pc_status pc_embed_q8(const void *d_tokens, int token_bytes, size_t n, const pc_
  *   d_grad    vocab x dim, row distance ld_grad.
  *   d_ws, ws_bytes  scratch of pc_embed_backward_workspace_bytes (0 for few
  *             tokens, then d_ws may be NULL), 16-byte aligned.
- * n below 2^31, vocab at most 2^31.
+ * Limits: with b = ceil(n / 32) ceil(dim / 512) (ceil(n / 8) in place of
+ * ceil(n / 32) where n ceil(dim / 512) is at most 32768), b - ceil(dim / 512)
+ * below 2^24 and b + vocab at most 2^26 - 4; n x dim and vocab x dim of at
+ * most 2^36 - 4096 elements each, dim counted in whole 32s.  Beyond them
+ * PC_ERR_UNSUPPORTED, and 0 bytes of workspace.
  */
 size_t pc_embed_backward_workspace_bytes(size_t n, size_t dim, size_t vocab);
 pc_status pc_embed_backward(const void *d_dy, int dy_dtype, size_t ld_dy, const void *d_tokens, int token_bytes,

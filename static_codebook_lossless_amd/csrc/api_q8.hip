@@ -144,8 +144,13 @@ pc_status pc_embed_q8(const void *d_tokens, int token_bytes, size_t n, const pc_
                          stream);
 }
 
+static bool embed_backward_size_ok(size_t n, size_t dim, size_t vocab) {
+    return n < kMaxWidth && vocab <= kMaxWidth && size_ok(n, dim) && size_ok(vocab, dim) &&
+           pc::embed_backward_fits(n, dim, vocab);
+}
+
 size_t pc_embed_backward_workspace_bytes(size_t n, size_t dim, size_t vocab) {
-    if (n >= kMaxWidth || vocab > kMaxWidth || dim >= kMaxWidth || !size_ok(n, dim) || !size_ok(vocab, dim)) return 0;
+    if (dim == 0 || vocab == 0 || !embed_backward_size_ok(n, dim, vocab)) return 0;
     return pc::embed_backward_workspace(n, dim, vocab);
 }
 
@@ -160,9 +165,7 @@ pc_status pc_embed_backward(const void *d_dy, int dy_dtype, size_t ld_dy, const 
     if (n && (!plain_ok(d_dy, dy_dtype, dim, ld_dy) || !d_tokens ||
               (reinterpret_cast<uintptr_t>(d_tokens) & (token_bytes - 1))))
         return PC_ERR_INVALID_ARG;
-    // the sums take at most a wave for every 8 sorted tokens and 512 columns, the zeros one for every row
-    if (n >= kMaxWidth || vocab > kMaxWidth || !size_ok(n, dim) || !size_ok(vocab, dim) || !span_ok(vocab, ld_grad) ||
-        (n && !span_ok(n, ld_dy)) || (n + 7) / 8 * ((dim + 511) / 512) + vocab / 4 >= kMaxGroups || (dim + 511) / 512 > 65535)
+    if (!embed_backward_size_ok(n, dim, vocab) || !span_ok(vocab, ld_grad) || (n && !span_ok(n, ld_dy)))
         return PC_ERR_UNSUPPORTED;
     const size_t need = pc_embed_backward_workspace_bytes(n, dim, vocab);
     if (need) {

@@ -633,6 +633,15 @@ uint64_t up16(uint64_t b) { return (b + 15) / 16 * 16; }
 
 }  // namespace
 
+// The sums take a wave for every block of sorted tokens and slab of columns,
+// and one for every row's zeros; the joins a workgroup for every block's end.
+bool embed_backward_fits(uint64_t n, uint64_t dim, uint64_t vocab) {
+    constexpr uint64_t kMaxGroups = (1ull << 24) - 1;  // of 256 lanes, in a launch of fewer than 2^32
+    if (is_small(n, vocab, dim)) return true;
+    const uint64_t slabs = slabs_of(dim), block = block_of(n, slabs), blocks = (n + block - 1) / block;
+    return (blocks * slabs + vocab + 3) / 4 <= kMaxGroups && (blocks == 0 || (blocks - 1) * slabs <= kMaxGroups);
+}
+
 uint64_t embed_backward_workspace(uint64_t n, uint64_t dim, uint64_t vocab) {
     if (is_small(n, vocab, dim)) return 0;
     const uint64_t block = block_of(n, slabs_of(dim)), blocks = (n + block - 1) / block;

@@ -126,6 +126,8 @@ hipError_t launch_embed(const void *tokens, int token_bytes, uint64_t n, const v
                         int kind, uint64_t vocab, uint64_t dim, uint64_t ld_table, uint64_t ld_codes, float scale,
                         void *out, int out_dtype, uint64_t ld_out, uint32_t *status, hipStream_t stream);
 
+// Whether the launches of this size are possible.
+bool embed_backward_fits(uint64_t n, uint64_t dim, uint64_t vocab);
 uint64_t embed_backward_workspace(uint64_t n, uint64_t dim, uint64_t vocab);
 hipError_t launch_embed_backward(const void *dy, int dtype, uint64_t ld_dy, const void *tokens, int token_bytes,
                                  uint32_t n, uint64_t dim, uint64_t vocab, int64_t padding, float scale, void *grad,

@@ -67,3 +67,33 @@ def test_rows_without_a_token_are_zero_for_every_scale(n, vocab, dim, scale):
     old = torch.full((vocab, dim), 4.0, device=DEV)
     pc.pc_embed_backward(dy, torch.from_numpy(tokens).to(DEV), vocab, scale=scale, out=old, accumulate=True)
     assert torch.all(old[torch.from_numpy(none).to(DEV)] == 4.0)
+
+
+def test_embed_backward_of_many_tokens():
+    # 2^28 tokens, a gradient of whole numbers that 32 bits hold
+    g = torch.Generator(device=DEV).manual_seed(9)
+    n, vocab = (1 << 28) + 5, 1000
+    tokens = torch.randint(0, vocab, (n,), generator=g, device=DEV, dtype=torch.int32)
+    dy = torch.randint(0, 4, (n,), generator=g, device=DEV, dtype=torch.int32)
+    want = torch.zeros(vocab, dtype=torch.int64, device=DEV)
+    for i in range(0, n, 1 << 26):
+        both = torch.bincount(tokens[i:i + (1 << 26)] * 4 + dy[i:i + (1 << 26)], minlength=4 * vocab).view(vocab, 4)
+        want += (both * torch.arange(4, device=DEV)).sum(1)
+    got = pc.pc_embed_backward(dy.to(torch.bfloat16).view(n, 1), tokens, vocab)
+    assert torch.equal(got.view(-1).long(), want)
+
+
+def test_embed_backward_to_the_tallest_and_the_widest_table():
+    dy = torch.tensor([[1.0], [2.0], [4.0], [8.0]], device=DEV)
+    for vocab in ((1 << 26) - 5, (1 << 25) + 1):
+        tokens = torch.tensor([vocab - 1, 0, vocab - 1, vocab // 2], device=DEV)
+        got = pc.pc_embed_backward(dy, tokens, vocab)
+        assert got[vocab - 1].item() == 5.0 and got[0].item() == 2.0 and got[vocab // 2].item() == 8.0
+        assert torch.count_nonzero(got).item() == 3
+        del got
+    dim = 65537 * 512 - 3  # more slabs of columns than a launch has rows of workgroups
+    wide = torch.ones(3, dim, device=DEV)
+    wide[1, dim - 1] = 5.0
+    got = pc.pc_embed_backward(wide, torch.tensor([1, 1, 3], device=DEV), 4)
+    assert torch.all(got[0] == 0) and torch.all(got[2] == 0) and torch.all(got[3] == 1)
+    assert torch.all(got[1, :-1] == 2) and got[1, -1].item() == 6.0

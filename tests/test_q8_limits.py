@@ -1,0 +1,26 @@
+"""The size limits of the stored-tensor and embedding operators, on the CPU,
+just inside and just outside.  A size inside is recognised by a later refusal
+(no workspace): no call here reaches the device."""
+import pytest
+
+import static_codebook_lossless_amd as pc
+from test_q8_args import A, BAD, BIG, back
+
+MI = 1 << 20
+
+
+@pytest.mark.parametrize("n,dim,vocab", [
+    (512 * MI, 1, 10), (512 * MI, 96, 10), (5, 1, 64 * MI - 5), (256 * MI, 1, 56 * MI - 4), (0, 1, 64 * MI - 4),
+    (128 * MI - 8, 512, 10), (3000, 1 << 24, 10), (600, 1 << 26, 3)])
+def test_embed_backward_accepts(n, dim, vocab):
+    assert pc.pc_embed_backward_workspace_bytes(n, dim, vocab) > 0
+    assert back(n=n, dim=dim, vocab=vocab, ld=dim, ldg=dim, ws=None, wsb=0) == BAD
+    assert back(n=n, dim=dim, vocab=vocab, ld=dim, ldg=dim, ws=A, wsb=16) == pc.PC_ERR_CAPACITY
+
+
+@pytest.mark.parametrize("n,dim,vocab", [
+    (512 * MI + 1, 1, 10), (5, 1, 64 * MI - 4), (256 * MI, 1, 56 * MI - 3), (0, 1, 64 * MI - 3), (128 * MI, 512, 10),
+    (512 * MI, 128, 10), (5, 1 << 16, 1 << 20), (1 << 31, 64, 10)])
+def test_embed_backward_refuses_what_it_cannot_launch(n, dim, vocab):
+    assert pc.pc_embed_backward_workspace_bytes(n, dim, vocab) == 0
+    assert back(n=n, dim=dim, vocab=vocab, ld=dim, ldg=dim) == BIG
