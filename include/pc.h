@@ -429,8 +429,9 @@ pc_status pc_q8_glu_backward(const void *d_dh, int dtype, size_t ld_dh, const pc
  * three times the operations).
  *   d_ws, ws_bytes  scratch of pc_q8_weight_grad_workspace_bytes (which may
  *             be 0, then d_ws may be NULL), 16-byte aligned.
- * x->rows == 0: dW = 0, or stays where accumulate.  Row distances of dy and
- * x of 2^24 elements and more: PC_ERR_UNSUPPORTED.
+ * x->rows == 0: dW = 0, or stays where accumulate.  PC_ERR_UNSUPPORTED: row
+ * distances of dy and x of 2^24 elements and more, and a dW of 2^24 - 7 tiles
+ * of 128 x 128 (256 x 256 where those are 160 and dy is bf16) and more.
  */
 size_t pc_q8_weight_grad_workspace_bytes(size_t rows, size_t n_out, size_t n_in, int dy_dtype);
 pc_status pc_q8_weight_grad(const void *d_dy, int dy_dtype, size_t ld_dy, size_t n_out, const pc_q8 *x, void *d_dw,

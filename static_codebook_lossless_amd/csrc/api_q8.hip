@@ -98,6 +98,7 @@ pc_status pc_q8_weight_grad(const void *d_dy, int dy_dtype, size_t ld_dy, size_t
     if (!plain_ok(d_dw, dw_dtype, n_in, ld_dw)) return PC_ERR_INVALID_ARG;
     if (rows && (!plain_ok(d_dy, dy_dtype, n_out, ld_dy) || !stored_ok(x))) return PC_ERR_INVALID_ARG;
     if (!size_ok(n_out, n_in) || !size_ok(rows, n_out) || !size_ok(rows, n_in) || !span_ok(n_out, ld_dw) ||
+        !pc::wgrad_fits(rows, n_out, n_in, dy_dtype) ||
         (rows && (!span_ok(rows, ld_dy) || !span_ok(rows, x->ld_sym) || !span_ok(rows, x->ld_scale))))
         return PC_ERR_UNSUPPORTED;
     if (rows && (ld_dy >= kMaxDistance || x->ld_sym >= kMaxDistance || x->ld_scale >= kMaxDistance))

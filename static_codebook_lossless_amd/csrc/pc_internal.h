@@ -117,6 +117,7 @@ hipError_t launch_q8_glu_backward(const void *dh, int dtype, uint64_t ld_dh, con
                                   int act, void *d_gate, uint64_t ld_gate, void *d_up, uint64_t ld_up, void *h,
                                   uint64_t ld_h, hipStream_t stream);
 
+bool wgrad_fits(uint64_t t, uint64_t n, uint64_t k, int dy_dtype);
 uint64_t wgrad_workspace(uint64_t t, uint64_t n, uint64_t k, int dy_dtype);
 hipError_t launch_q8_weight_grad(const void *dy, int dtype, uint64_t ld_dy, uint64_t n_out, const pc_q8 *x, void *dw,
                                  int dw_dtype, uint64_t ld_dw, bool accumulate, void *ws, hipStream_t stream);

@@ -563,6 +563,11 @@ uint64_t wgrad_workspace(uint64_t t, uint64_t n, uint64_t k, int dtype) {
     return p.slices > 1 ? (uint64_t)p.slices * n * k * 4 : 0;
 }
 
+// The launch takes a workgroup for every tile, a multiple of 8 of them, and fewer than 2^24.
+bool wgrad_fits(uint64_t t, uint64_t n, uint64_t k, int dtype) {
+    return tiles_of(n, k, plan_of(t, n, k, dtype).side) + 7 < 1ull << 24;
+}
+
 hipError_t launch_q8_weight_grad(const void *dy, int dtype, uint64_t ld_dy, uint64_t n_out, const pc_q8 *x, void *dw,
                                  int dw_dtype, uint64_t ld_dw, bool accumulate, void *ws, hipStream_t stream) {
     const uint64_t t = x->rows, n = n_out, k = x->cols;

@@ -97,3 +97,14 @@ def test_embed_backward_to_the_tallest_and_the_widest_table():
     got = pc.pc_embed_backward(wide, torch.tensor([1, 1, 3], device=DEV), 4)
     assert torch.all(got[0] == 0) and torch.all(got[2] == 0) and torch.all(got[3] == 1)
     assert torch.all(got[1, :-1] == 2) and got[1, -1].item() == 6.0
+
+
+def test_weight_grad_of_no_rows_to_the_widest_result():
+    k = (1 << 31) - 1024  # 2^24 - 8 tiles
+    x = pc.Q8(torch.empty((0, k), dtype=torch.uint8, device=DEV), torch.empty((0, k // 32), dtype=torch.uint8, device=DEV))
+    out = torch.full((1, k), 3.0, dtype=torch.bfloat16, device=DEV)
+    none = torch.empty((0, 1), dtype=torch.float32, device=DEV)
+    pc.pc_q8_weight_grad(none, x, dtype=torch.bfloat16, out=out, accumulate=True)
+    assert torch.all(out == 3.0)
+    pc.pc_q8_weight_grad(none, x, dtype=torch.bfloat16, out=out)
+    assert torch.all(out == 0.0)

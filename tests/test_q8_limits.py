@@ -4,7 +4,7 @@ just inside and just outside.  A size inside is recognised by a later refusal
 import pytest
 
 import static_codebook_lossless_amd as pc
-from test_q8_args import A, BAD, BIG, back
+from test_q8_args import A, BAD, BIG, back, q8, wgrad
 
 MI = 1 << 20
 
@@ -24,3 +24,9 @@ def test_embed_backward_accepts(n, dim, vocab):
 def test_embed_backward_refuses_what_it_cannot_launch(n, dim, vocab):
     assert pc.pc_embed_backward_workspace_bytes(n, dim, vocab) == 0
     assert back(n=n, dim=dim, vocab=vocab, ld=dim, ldg=dim) == BIG
+
+
+@pytest.mark.parametrize("n,k", [(1, (1 << 31) - 1), ((1 << 31) - 128, 1)])
+def test_weight_grad_of_no_rows_refuses_what_it_cannot_launch(n, k):
+    # 2^24 tiles of 256 lanes: no launch holds them, also where they only write zeros
+    assert wgrad(x=q8(rows=0, cols=k), dtype=pc.PC_F32, n=n, ld=n, ldw=k) == BIG
