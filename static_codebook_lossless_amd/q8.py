@@ -11,6 +11,7 @@ distance (``view(-1, cols)``).  Wrong types, sizes, strides or devices raise
 from __future__ import annotations
 
 import math
+import operator
 
 import torch
 
@@ -136,7 +137,12 @@ class Q8:
 
     def with_symbols(self, symbols):
         """The same tensor with its symbols in other memory (decoded bytes)."""
-        return Q8(symbols.view(self.symbols.shape), self.scales, self.format)
+        try:
+            symbols = symbols.view(self.symbols.shape)
+        except RuntimeError:
+            raise ValueError("symbols of %s cannot be seen as %s"
+                             % (list(symbols.shape), list(self.symbols.shape))) from None
+        return Q8(symbols, self.scales, self.format)
 
     def columns(self, begin, end):
         """A view of columns [begin, end); begin is a multiple of 32."""
@@ -145,6 +151,11 @@ class Q8:
             raise ValueError("columns begin and end at multiples of 32 (or at the tensor's end)")
         return Q8(self.symbols[:, begin:end], self.scales[:, begin // PC_Q8_GROUP:-(-end // PC_Q8_GROUP)],
                   self.format)
+
+
+def _stored(q, what):
+    if not isinstance(q, Q8):
+        raise TypeError("%s must be a Q8, not %s" % (what, type(q).__name__))
 
 
 def pc_q8_store(x, format="e4m3", counts=None) -> Q8:
@@ -184,6 +195,7 @@ def _output(out, shape, dtype, device, what="out"):
 
 def pc_q8_load(q: Q8, dtype=torch.bfloat16, out=None) -> torch.Tensor:
     """The values of a stored tensor, rounded to ``dtype`` (``out``: where to, of that dtype)."""
+    _stored(q, "q")
     kind = _dtype(dtype, "dtype")
     out, ld = _output(out, tuple(q.symbols.shape), dtype, q.device)
     _launch("pc_q8_load", q.device, lib.pc_q8_load, q.arg, out.data_ptr(), kind, ld)
@@ -217,6 +229,9 @@ def pc_q8_glu_backward(dh, gate: Q8, up: Q8 | None = None, act="silu", with_h=Fa
     columns is an activation without a gate, ``h = act(gate)``.  Gradients and
     ``h`` are [rows, cols] of dh's dtype (a dh of more dimensions counts as
     rows of its last one)."""
+    _stored(gate, "gate")
+    if up is not None:
+        _stored(up, "up")
     kind, a = _dtype(dh.dtype, "dh"), _code(_ACTS, act, "act")
     x, ld = _rows(dh, "dh")
     rows, cols = x.shape
@@ -263,6 +278,7 @@ def pc_q8_weight_grad_workspace_bytes(rows, n_out, n_in, dy_dtype=PC_BF16):
 def pc_q8_weight_grad(dy, x: Q8, dtype=torch.float32, out=None, accumulate=False) -> torch.Tensor:
     """``dy^T @ x`` for a stored ``x``: [n_out, n_in] of ``dtype``.  ``out``
     (of that dtype) receives it; with ``accumulate`` it is added there."""
+    _stored(x, "x")
     kind, out_kind = _dtype(dy.dtype, "dy"), _dtype(dtype, "dtype")
     dy, ld = _rows(dy, "dy")
     _same_device(dy, x.symbols, "x")
@@ -294,7 +310,7 @@ def pc_embed(tokens, table, scale=1.0, dtype=None, out=None, status=None) -> tor
     [vocab, dim], plain or a ``Q8``.  A token outside the table gives a row
     of zeros and, where ``status`` (int32 [1] on the device, zeroed by the
     caller) is given, sets it to ``PC_ERR_INVALID_ARG``."""
-    stored = isinstance(table, Q8)
+    stored, scale = isinstance(table, Q8), float(scale)
     rows, ld = (table.symbols, 0) if stored else _rows(table, "table")
     if not stored and table.dim() != 2:
         raise ValueError("table must have two dimensions")
@@ -327,8 +343,7 @@ def pc_embed(tokens, table, scale=1.0, dtype=None, out=None, status=None) -> tor
 
 def pc_embed_q8(tokens, table: Q8, scale=1.0, dtype=torch.bfloat16, out=None, status=None) -> torch.Tensor:
     """``pc_embed`` of a stored table."""
-    if not isinstance(table, Q8):
-        raise TypeError("table must be a Q8")
+    _stored(table, "table")
     return pc_embed(tokens, table, scale, dtype, out, status)
 
 
@@ -343,6 +358,7 @@ def pc_embed_backward(dy, tokens, vocab, scale=1.0, dtype=torch.float32, padding
     outside the table or equal to ``padding`` add nothing.  ``out`` (of that
     dtype) receives it; with ``accumulate`` it is added there."""
     kind, out_kind = _dtype(dy.dtype, "dy"), _dtype(dtype, "dtype")
+    scale, padding = float(scale), operator.index(padding)
     if dy.shape[:-1] != tokens.shape:
         raise ValueError("dy must be [*tokens.shape, dim]")
     dy, ld = _rows(dy, "dy")

@@ -108,3 +108,23 @@ def test_weight_grad_of_no_rows_to_the_widest_result():
     assert torch.all(out == 3.0)
     pc.pc_q8_weight_grad(none, x, dtype=torch.bfloat16, out=out)
     assert torch.all(out == 0.0)
+
+
+def test_the_binding_takes_numbers_and_refuses_others():
+    table, tokens = torch.ones(5, 8, device=DEV), torch.tensor([1, 4], device=DEV)
+    for scale in (2, 2.0, np.float32(2), torch.tensor(2.0)):
+        assert torch.all(pc.pc_embed(tokens, table, scale=scale) == 2)
+        assert pc.pc_embed_backward(table[:2], tokens, 5, scale=scale, padding=np.int64(4)).sum().item() == 16
+    for call in (lambda: pc.pc_embed(tokens, table, scale="two"), lambda: pc.pc_embed(tokens, table, scale=None),
+                 lambda: pc.pc_embed_backward(table[:2], tokens, 5, scale=[2]),
+                 lambda: pc.pc_embed_backward(table[:2], tokens, 5, padding=0.5)):
+        with pytest.raises((TypeError, ValueError)):
+            call()
+    q = pc.pc_q8_store(torch.randn(6, 70, device=DEV))
+    wide = torch.zeros(6, 100, dtype=torch.uint8, device=DEV)
+    wide[:, 5:75].copy_(q.symbols)
+    for symbols in (q.symbols.reshape(-1), q.symbols.view(2, 3, 70), wide[:, 5:75], wide.view(2, 3, 100)[:, :, 5:75]):
+        assert torch.equal(pc.pc_q8_load(q.with_symbols(symbols)), pc.pc_q8_load(q))
+    for symbols in (q.symbols.reshape(-1)[:-1], q.symbols.t(), wide):
+        with pytest.raises(ValueError):
+            q.with_symbols(symbols)

@@ -2,6 +2,7 @@
 just inside and just outside.  A size inside is recognised by a later refusal
 (no workspace): no call here reaches the device."""
 import pytest
+import torch
 
 import static_codebook_lossless_amd as pc
 from test_q8_args import A, BAD, BIG, back, q8, wgrad
@@ -30,3 +31,22 @@ def test_embed_backward_refuses_what_it_cannot_launch(n, dim, vocab):
 def test_weight_grad_of_no_rows_refuses_what_it_cannot_launch(n, k):
     # 2^24 tiles of 256 lanes: no launch holds them, also where they only write zeros
     assert wgrad(x=q8(rows=0, cols=k), dtype=pc.PC_F32, n=n, ld=n, ldw=k) == BIG
+
+
+def test_binding_raises_type_and_value_errors():
+    s, c = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.uint8)
+    q = pc.Q8._dense(s, c, "e4m3", 4, 64, 0)  # in host memory, where only the checks are reached
+    with pytest.raises(ValueError):
+        q.with_symbols(torch.zeros(255, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        q.with_symbols(torch.zeros(8, 64, dtype=torch.uint8)[::2].t())
+    x = torch.zeros(4, 64)
+    for call in (lambda: pc.pc_q8_load(x), lambda: pc.pc_q8_glu_backward(x, x), lambda: pc.pc_q8_glu_backward(x, q, x),
+                 lambda: pc.pc_q8_weight_grad(x, x), lambda: pc.pc_embed_q8(torch.zeros(3, dtype=torch.int64), x)):
+        with pytest.raises(TypeError, match="must be a Q8"):
+            call()
+    tokens = torch.zeros(4, dtype=torch.int64)
+    with pytest.raises((TypeError, ValueError)):
+        pc.pc_embed(tokens, x, scale="two")
+    with pytest.raises(TypeError):
+        pc.pc_embed_backward(x, tokens, 10, padding=None)
