@@ -343,9 +343,10 @@ pc_status pc_traffic_probe(const void *d_src, void *d_dst, size_t bytes, void *s
  *          element(sym[r][c]) * 2^(scale[r][c / 32] - 127),
  * element() being OCP E4M3FN or int8 two's complement.  A byte that stands
  * for no number (0x7F and 0xFF in e4m3, 0x80 in int8) reads as NaN.  Powers
- * of two keep every stored value exact in bf16 and f32, so the matrix
- * instructions multiply stored values without rounding them again.  Scale
- * codes run from 1 to 254; pc_q8_store writes 10 to 249.
+ * of two keep stored values exact in bf16 and f32, so the matrix instructions
+ * multiply them without rounding them again.  Scale codes run from 1 to 254;
+ * pc_q8_store writes 10 to 249, under which only 2^128 and more, as infinity,
+ * leaves the range of bf16 and f32.
  *
  * Tensors of plain numbers are f32, f16 or bf16, rows of unit stride and a
  * row distance `ld` in elements that may exceed the width; pointers need the
@@ -386,8 +387,11 @@ typedef struct pc_q8 {
  * the largest finite magnitude in it and M the format's (448 or 127):
  *   k = the smallest integer >= -117 with a <= M 2^k  (-117 where a is 0)
  *   sym = x 2^-k rounded to the nearest element, ties to even;  code = k + 127
- * so no finite value saturates.  Infinities and NaN take no part in a and
- * become 0x7F (e4m3) or 0x80 (int8), which read back as NaN.
+ * so no finite value saturates.  Magnitudes from 248 * 2^120 on (e4m3; int8:
+ * above 127 * 2^121, and from it on beside such a one), the largest finite
+ * f32 and bf16 among them, round to 2^128 and so read back as infinity.
+ * Infinities and NaN take no part in a and become 0x7F (e4m3) or 0x80 (int8),
+ * which read back as NaN.
  *   d_x       rows x cols, row distance ldx.
  *   d_sym     rows * cols bytes, dense.
  *   d_scale   rows * ceil(cols / 32) bytes, dense.
@@ -426,7 +430,8 @@ pc_status pc_q8_glu_backward(const void *d_dh, int dtype, size_t ld_dh, const pc
  * Products are exact and sums are in 32 bits: stored values and bf16
  * gradients go into bf16 matrix instructions as they are; f16 and f32
  * gradients go in as two and three bf16 terms that add up to them (two and
- * three times the operations).
+ * three times the operations; of f32 gradients below 2^-110 what lies below
+ * 2^-133, bf16's smallest step, is lost).
  *   d_ws, ws_bytes  scratch of pc_q8_weight_grad_workspace_bytes (which may
  *             be 0, then d_ws may be NULL), 16-byte aligned.
  * x->rows == 0: dW = 0, or stays where accumulate.  PC_ERR_UNSUPPORTED: row

@@ -162,7 +162,9 @@ def pc_q8_store(x, format="e4m3", counts=None) -> Q8:
     """Store ``x`` in 8 bits with one scale for every 32 columns.  ``counts``
     (int64 [256] on the device) gets the histogram of the symbols added, in
     the same pass.  x of more than two dimensions is stored as rows of its
-    last one.  Infinities and NaN read back as NaN."""
+    last one.  Infinities and NaN read back as NaN; finite magnitudes that
+    round to 2**128 (the largest finite float32 and bfloat16 do) read back as
+    infinity."""
     code, kind = _code(_FORMATS, format, "format"), _dtype(x.dtype, "x")
     x, ld = _rows(x, "x")
     rows, cols = x.shape

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from oracle import q8
-from test_gpu_q8 import DEV, _need_gpu, activation, make_q8, np64  # noqa: F401
+from test_gpu_q8 import DEV, DT, _need_gpu, activation, make_q8, np64, rounded, same, tensor  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +128,45 @@ def test_the_binding_takes_numbers_and_refuses_others():
     for symbols in (q.symbols.reshape(-1)[:-1], q.symbols.t(), wide):
         with pytest.raises(ValueError):
             q.with_symbols(symbols)
+
+
+# -- the ends of the range ------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt,limit", [("e4m3", 248 * 2.0 ** 120), ("int8", 127 * 2.0 ** 121)])
+def test_the_top_of_the_range_rounds_to_infinity(fmt, limit):
+    # magnitudes that round to 2^128 are stored as that, which 32 bits read as
+    # infinity; below them everything is finite
+    below = float(np.nextafter(np.float32(limit), np.float32(0)))
+    most, most_bf16 = float(np.finfo(np.float32).max), 255 * 2.0 ** 120
+    rows = [[v] + [1.0] * 31 for v in (below, most_bf16, -most_bf16, most, -most)]
+    rows.append([most, below, -below, limit] + [0.0] * 28)
+    x = np.array(rows, dtype=np.float32)
+    q = pc.pc_q8_store(torch.from_numpy(x).to(DEV), fmt)
+    sym, codes = q8.store(x.astype(np.float64), fmt)
+    assert np.array_equal(q.symbols.cpu().numpy(), sym) and np.array_equal(q.scales.cpu().numpy(), codes)
+    v = q8.load(sym, codes, fmt)
+    assert np.array_equal(np.abs(v) == 2.0 ** 128, (np.abs(x) > limit) | ((x == limit) & (np.arange(32) == 3)))
+    for to in ("f32", "bf16"):
+        same(np64(pc.pc_q8_load(q, DT[to])), rounded(v, to))
+    dy = np.zeros((6, 8), dtype=np.float32)
+    dy[:, 0] = [1, 0, 0, 0, 0, 0]
+    dy[:, 1] = [0, 1, 0, 0, 0, 0]
+    with np.errstate(invalid="ignore"):
+        want = dy.astype(np.float64).T @ rounded(v, "f32")
+    for dtype in ("bf16", "f32"):
+        same(np64(pc.pc_q8_weight_grad(tensor(dy, dtype), q)), rounded(want, "f32"))
+
+
+def test_weight_grad_of_the_smallest_numbers():
+    # the three terms of a 32-bit gradient are bf16 numbers, whose smallest
+    # step is 2^-133: what lies below that is lost
+    rng = np.random.default_rng(34)
+    sym, codes = q8.store(rng.normal(size=(40, 64)) * 2.0 ** 60, "int8")
+    q = pc.Q8(torch.from_numpy(sym).to(DEV), torch.from_numpy(codes).to(DEV), "int8")
+    x = q8.load(sym, codes, "int8")
+    for scale in (2.0 ** -100, 2.0 ** -112, 2.0 ** -122, 2.0 ** -130):
+        dy = (rng.normal(size=(40, 24)) * scale).astype(np.float32)
+        want, size = q8.weight_grad(dy.astype(np.float64), x), np.abs(dy.astype(np.float64)).T @ np.abs(x)
+        lost = 2.0 ** -133 * np.abs(x).sum(axis=0)[None, :]
+        off = np.abs(np64(pc.pc_q8_weight_grad(tensor(dy, "f32"), q)) - want)
+        assert np.all(off <= 43 * 2.0 ** -23 * size + lost), (scale, float((off / size).max()))
