@@ -1,6 +1,11 @@
 """Edges of the stored-tensor and embedding operators on the GPU: the ends of
-their number ranges, against 64-bit forms.  Tolerances were fixed before the
-first run and are derived where they are used.
+their number ranges, the sizes at which their launches change, and operands
+past 4 GiB, against 64-bit forms.
+
+Tolerances, fixed before the first run: as in test_gpu_q8.py, sums of m exact
+terms in 32 bits are off by at most (m + 2) 2^-23 times the sum of the terms'
+magnitudes, plus half a step of the output's type; others are derived where
+they are used.
 """
 import math
 
@@ -9,7 +14,8 @@ import pytest
 import torch
 
 from oracle import q8
-from test_gpu_q8 import DEV, DT, _need_gpu, activation, make_q8, np64, rounded, same, tensor  # noqa: F401
+from test_gpu_q8 import (DEV, DT, HALF_STEP, TINY, _need_gpu, activation, check_glu, check_wgrad,  # noqa: F401
+                         make_q8, np64, rounded, same, say, tensor)
 
 pytestmark = pytest.mark.gpu
 
@@ -101,7 +107,8 @@ def test_embed_backward_to_the_tallest_and_the_widest_table():
 
 def test_weight_grad_of_no_rows_to_the_widest_result():
     k = (1 << 31) - 1024  # 2^24 - 8 tiles
-    x = pc.Q8(torch.empty((0, k), dtype=torch.uint8, device=DEV), torch.empty((0, k // 32), dtype=torch.uint8, device=DEV))
+    x = pc.Q8(torch.empty((0, k), dtype=torch.uint8, device=DEV),
+              torch.empty((0, k // 32), dtype=torch.uint8, device=DEV))
     out = torch.full((1, k), 3.0, dtype=torch.bfloat16, device=DEV)
     none = torch.empty((0, 1), dtype=torch.float32, device=DEV)
     pc.pc_q8_weight_grad(none, x, dtype=torch.bfloat16, out=out, accumulate=True)
@@ -170,3 +177,137 @@ def test_weight_grad_of_the_smallest_numbers():
         lost = 2.0 ** -133 * np.abs(x).sum(axis=0)[None, :]
         off = np.abs(np64(pc.pc_q8_weight_grad(tensor(dy, "f32"), q)) - want)
         assert np.all(off <= 43 * 2.0 ** -23 * size + lost), (scale, float((off / size).max()))
+
+
+# -- the sizes at which launches change, and operands past 4 GiB ----------------------
+
+def test_glu_backward_of_stored_views():
+    rng = np.random.default_rng(31)
+    both, v = make_q8(rng, 6, 256, "int8", 2.0)
+    dh = tensor(rng.normal(size=(6, 64)).astype(np.float32), "f32")
+    gate, up = both.columns(32, 96), both.columns(160, 224)
+    check_glu(np64(dh), v[:, 32:96], v[:, 160:224], "silu", "f32", pc.pc_q8_glu_backward(dh, gate, up))
+    middle = both.columns(64, 192)  # gate and up side by side inside a wider tensor
+    r = pc.pc_q8_glu_backward(dh, middle, with_h=True)
+    check_glu(np64(dh), v[:, 64:128], v[:, 128:192], "silu", "f32", r, r.h)
+    out = pc.pc_embed(torch.tensor([5, 0, 5], device=DEV), middle, dtype=torch.float32)
+    same(np64(out), v[[5, 0, 5], 64:192])
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("dtype,rows,cols", [("bf16", 2600, 2049), ("f32", 2600, 2049), ("bf16", 2600, 2048),
+                                             ("f16", 20000, 250)])
+def test_counted_store_in_several_rounds(dtype, rows, cols, fmt):
+    # a counting workgroup takes 2048 units of 8 columns at a time, and 256 of
+    # them 4 Mi elements a round: the last round here is a partial one
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.randn(rows, cols, generator=g, device=DEV).mul_(3.0).to(DT[dtype])
+    x[7, 3], x[rows - 1, cols - 1] = math.nan, math.inf
+    counts = torch.full((256,), 5, dtype=torch.int64, device=DEV)
+    q, plain = pc.pc_q8_store(x, fmt, counts=counts), pc.pc_q8_store(x, fmt)
+    assert torch.equal(q.symbols, plain.symbols) and torch.equal(q.scales, plain.scales)
+    assert torch.equal(counts - 5, torch.bincount(q.symbols.reshape(-1), minlength=256))
+    for at in (slice(0, 9), slice(rows // 2, rows // 2 + 9), slice(rows - 9, rows)):
+        sym, codes = q8.store(np64(x[at]), fmt)
+        assert np.array_equal(q.symbols[at].cpu().numpy(), sym) and np.array_equal(q.scales[at].cpu().numpy(), codes)
+
+
+@pytest.mark.parametrize("odt", ["f16", "bf16"])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_weight_grad_in_slices_to_16_bits(dtype, odt):
+    rng = np.random.default_rng(32)
+    q, x = make_q8(rng, 3001, 65, "e4m3", 0.1)
+    dy = tensor(rng.normal(size=(3001, 31)).astype(np.float32) * 0.1, dtype)
+    assert pc.pc_q8_weight_grad_workspace_bytes(3001, 31, 65) > 0
+    check_wgrad(np64(dy), x, pc.pc_q8_weight_grad(dy, q, dtype=DT[odt]), odt)
+    old = tensor(rng.normal(size=(31, 65)).astype(np.float32), odt)
+    out = old.clone()
+    pc.pc_q8_weight_grad(dy, q, dtype=DT[odt], out=out, accumulate=True)
+    check_wgrad(np64(dy), x, out, odt, np64(old))
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("n,k", [(100, 64), (104, 70)])
+def test_weight_grad_of_operands_past_4_gib(n, k, fmt):
+    # rows 32 MB and 16 MB apart: dy spans 10 GB, x 5 GB
+    rng = np.random.default_rng(33)
+    t, ld = 300, (1 << 24) - 8
+    dy = torch.zeros((t - 1) * ld + n, dtype=torch.bfloat16, device=DEV).as_strided((t, n), (ld, 1))
+    dy.copy_(activation(rng, t, n, "bf16"))
+    sym, codes = q8.store(rng.normal(size=(t, k)), fmt)
+    far = torch.zeros((t - 1) * ld + k, dtype=torch.uint8, device=DEV).as_strided((t, k), (ld, 1))
+    far.copy_(torch.from_numpy(sym))
+    q = pc.Q8(far, torch.from_numpy(codes).to(DEV), fmt)
+    check_wgrad(np64(dy), q8.load(sym, codes, fmt), pc.pc_q8_weight_grad(dy, q), "f32")
+
+
+def test_weight_grad_of_many_rows_past_4_gib():
+    # 5 GB of dy without gaps, its rows shared among slices
+    g = torch.Generator(device=DEV).manual_seed(6)
+    t, n, k = 2_500_033, 1000, 48
+    dy = torch.randn(t, n, generator=g, device=DEV, dtype=torch.bfloat16)
+    q = pc.pc_q8_store(torch.randn(t, k, generator=g, device=DEV), "e4m3")
+    got = pc.pc_q8_weight_grad(dy, q)
+    want, size = torch.zeros(n, k, dtype=torch.float64, device=DEV), torch.zeros(n, k, dtype=torch.float64, device=DEV)
+    for i in range(0, t, 1 << 18):
+        a = dy[i:i + (1 << 18)].double().t().contiguous()
+        b = pc.pc_q8_load(pc.Q8(q.symbols[i:i + (1 << 18)], q.scales[i:i + (1 << 18)]), torch.float32).double()
+        want += torch.mm(a, b)
+        size += torch.mm(a.abs_(), b.abs_())
+    # no sum is longer than a slice's and its join
+    assert bool((torch.abs(got.double() - want) <= (t + 3) * 2.0 ** -23 * size).all())
+    assert float((got.double() - want).norm() / want.norm()) < 1e-4
+
+
+def check_embed_backward(dy, tokens, vocab, odt="f32"):
+    got = pc.pc_embed_backward(dy, tokens, vocab, dtype=DT[odt])
+    dim = dy.shape[1]
+    want = torch.zeros(vocab, dim, dtype=torch.float64, device=DEV).index_add_(0, tokens, dy.double())
+    size = torch.zeros(vocab, dim, dtype=torch.float64, device=DEV).index_add_(0, tokens, dy.double().abs())
+    terms = torch.bincount(tokens, minlength=vocab).unsqueeze(1)
+    tol = (terms + 3) * 2.0 ** -23 * size
+    assert bool((torch.abs(got.double() - want) <= tol + HALF_STEP[odt] * want.abs() + TINY[odt] * (size > 0)).all())
+    assert torch.equal(got, pc.pc_embed_backward(dy, tokens, vocab, dtype=DT[odt]))
+    old = torch.ones(vocab, dim, dtype=DT[odt], device=DEV)
+    pc.pc_embed_backward(dy, tokens, vocab, dtype=DT[odt], out=old, accumulate=True)
+    off = torch.abs(old.double() - (want + 1))
+    assert bool((off <= tol + 2.0 ** -23 + HALF_STEP[odt] * (want + 1).abs()).all())
+    assert bool((old[(terms == 0).view(-1)] == 1).all())
+
+
+def some_tokens(g, n, vocab, skew):
+    u = torch.rand(n, generator=g, device=DEV, dtype=torch.float64)
+    if skew == "one":
+        return torch.where(u < 0.9, torch.full_like(u, vocab // 2), u * vocab).long().clamp_(max=vocab - 1)
+    return (u ** skew * vocab).long().clamp_(max=vocab - 1)
+
+
+@pytest.mark.parametrize("skew", [1, 8, "one"])
+@pytest.mark.parametrize("n", [511, 512, 513])
+def test_embed_backward_at_the_change_of_launches(n, skew):
+    # up to 512 tokens in one launch, of up to 16 rows of the table a workgroup; the last workgroup's range is short
+    g = torch.Generator(device=DEV).manual_seed(7)
+    for vocab, dim, dtype, odt in [(30001, 40, "bf16", "f32"), (15007, 601, "f32", "f32"), (34813, 512, "f16", "bf16"),
+                                   (34816, 8, "f32", "f32"), (6553, 2051, "bf16", "f16")]:
+        say("embed backward", n, vocab, dim, skew)
+        dy = torch.randn(n, dim, generator=g, device=DEV).to(DT[dtype])
+        check_embed_backward(dy, some_tokens(g, n, vocab, skew), vocab, odt)
+
+
+@pytest.mark.parametrize("skew", [1, 8, "one"])
+@pytest.mark.parametrize("dim", [2050, 2052])
+def test_embed_backward_of_many_joins(dim, skew):
+    # 1032 blocks of sorted tokens on 5 slabs of columns: 5155 ends of blocks that a run may cross
+    g = torch.Generator(device=DEV).manual_seed(8)
+    dy = torch.randn(33000, dim, generator=g, device=DEV).to(torch.bfloat16)
+    check_embed_backward(dy, some_tokens(g, 33000, 3001, skew), 3001)
+
+
+@pytest.mark.parametrize("dim", [7, 64, 1000])
+def test_embed_backward_of_nothing_to_a_large_table(dim):
+    none, no_tokens = torch.empty(0, dim, device=DEV), torch.empty(0, dtype=torch.int64, device=DEV)
+    out = torch.full((100_003, dim), 2.0, device=DEV)
+    pc.pc_embed_backward(none, no_tokens, 100_003, out=out, accumulate=True)
+    assert torch.all(out == 2.0)
+    pc.pc_embed_backward(none, no_tokens, 100_003, out=out)
+    assert torch.all(out == 0.0)
