@@ -46,7 +46,7 @@ __global__ __launch_bounds__(kThreads) void embed_kernel(const void *__restrict_
         n[j] = 0;
         if (base + local < units.total) {
             find_unit(units, base, local, row[j], col[j]);
-            if (col[j] < units.cols) n[j] = (uint32_t)min((uint64_t)kUnit, units.cols - col[j]);
+            n[j] = count_before(units.cols, col[j], kUnit);
             tok[j] = token_at<TOK>(tokens, row[j]);
         }
     }
@@ -95,7 +95,7 @@ template <bool WHOLE> struct Columns {
 #pragma unroll
         for (uint32_t q = 0; q < 2; ++q) {
             first[q] = slab * kSlab + q * 256 + lane * 4;
-            n[q] = first[q] < dim ? (uint32_t)min((uint64_t)4, dim - first[q]) : 0;
+            n[q] = count_before(dim, first[q], 4);
         }
     }
 };
@@ -521,7 +521,7 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(const typename Plain<DT>:
     const uint32_t count = uniform(in.start[vocab]);
     const uint32_t p0 = b * block;
     if (p0 >= count) return;
-    const uint32_t places = min(block, count - p0);
+    const uint32_t places = count_before(count, p0, block);
     // lane i: the key of place p0 + i - 1 (lane 0 the place before the block, if any), the row of place p0 + i
     const bool has = lane <= places + 1 && p0 + lane >= 1 && p0 + lane - 1 < count;
     const uint32_t key = has ? in.key[p0 + lane - 1] : ~0u;

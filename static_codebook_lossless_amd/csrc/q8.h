@@ -36,6 +36,17 @@ __device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ float widen(_Float16 v) { return (float)v; }
 __device__ __forceinline__ float widen(__bf16 v) { return as_f32((uint32_t)__builtin_bit_cast(uint16_t, v) << 16); }
 
+// How many of the `most` places from `at` on lie before `end`.  The difference
+// is one that is valid for every `at`:  of  at < end ? min(end - at, most) : 0
+// the compiler forms the minimum ahead of the test, takes at <= end as given
+// from there on, and drops other clamps that this would make needless (loads
+// then ran past the end of rows).
+template <class T>
+__device__ __forceinline__ uint32_t count_before(T end, T at, uint32_t most) {
+    const T past = at > end ? at : end, left = past - at;
+    return left < most ? (uint32_t)left : most;
+}
+
 // n (0..8) elements as loaded; the others 0.
 template <int DT> struct RawUnit { u32x4 w[DT == PC_F32 ? 2 : 1]; };
 

@@ -115,7 +115,7 @@ __global__ __launch_bounds__(COUNT ? kCountThreads : kThreads) void store_kernel
             if (base + local < units.total) {
                 find_unit(units, base, local, u[j].row, u[j].col);
                 // a short group's last units may hold no column at all
-                if (u[j].col < units.cols) u[j].n = (uint32_t)min((uint64_t)kUnit, units.cols - u[j].col);
+                u[j].n = count_before(units.cols, u[j].col, kUnit);
             }
             u[j].raw = load_raw<DT>(x + u[j].row * ldx + u[j].col, u[j].n);
         }
@@ -217,7 +217,7 @@ __global__ __launch_bounds__(kThreads) void load_kernel(const uint8_t *__restric
         n[j] = 0;
         if (base + local < units.total) {
             find_unit(units, base, local, row[j], col[j]);
-            if (col[j] < units.cols) n[j] = (uint32_t)min((uint64_t)kUnit, units.cols - col[j]);
+            n[j] = count_before(units.cols, col[j], kUnit);
         }
         if (n[j]) {
             w[j] = load_symbols(sym + row[j] * ld_sym + col[j], n[j]);
@@ -328,7 +328,7 @@ __global__ __launch_bounds__(kThreads) void glu_kernel(const typename Plain<DT>:
         n[j] = 0;
         if (base + local < units.total) {
             find_unit(units, base, local, row[j], col[j]);
-            if (col[j] < units.cols) n[j] = (uint32_t)min((uint64_t)kUnit, units.cols - col[j]);
+            n[j] = count_before(units.cols, col[j], kUnit);
         }
         if (n[j]) {
             const uint64_t r = row[j], c = col[j];

@@ -497,7 +497,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(const float *__restrict_
     __shared__ f32x4 sums[kShares][kWave];
     const uint32_t lane = threadIdx.x % kWave, share = threadIdx.x / kWave;
     const uint64_t all = n * k, i = ((uint64_t)blockIdx.x * kWave + lane) * 4;
-    const uint32_t have = i < all ? (uint32_t)min(all - i, (uint64_t)4) : 0;
+    const uint32_t have = count_before(all, i, 4);
     const uint32_t each = (slices + kShares - 1) / kShares, first = min(slices, share * each);
     const uint32_t end = min(slices, first + each);
     f32x4 sum = {0, 0, 0, 0};

@@ -311,3 +311,21 @@ def test_embed_backward_of_nothing_to_a_large_table(dim):
     assert torch.all(out == 2.0)
     pc.pc_embed_backward(none, no_tokens, 100_003, out=out)
     assert torch.all(out == 0.0)
+
+
+@pytest.mark.parametrize("n,vocab", [(300, 500), (5000, 300)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_embed_backward_of_rows_that_end_where_memory_ends(dtype, n, vocab):
+    # the last row's last column is the last of a 32 MiB allocation: nothing lies behind it
+    g = torch.Generator(device=DEV).manual_seed(10)
+    for dim in (4, 8, 33, 64, 252, 256, 260, 511, 516, 764, 1000):
+        say("embed backward", n, dim, vocab, dtype)
+        memory = torch.zeros((32 << 20) // DT[dtype].itemsize, dtype=DT[dtype], device=DEV)
+        dy = memory[-n * dim:].view(n, dim)
+        dy.copy_(torch.randn(n, dim, generator=g, device=DEV))
+        tokens = some_tokens(g, n, vocab, 4)
+        check_embed_backward(dy, tokens, vocab)
+        old = torch.zeros((32 << 20) // 4, device=DEV)[-vocab * dim:].view(vocab, dim)
+        pc.pc_embed_backward(dy, tokens, vocab, out=old, accumulate=True)
+        assert torch.equal(old, pc.pc_embed_backward(dy, tokens, vocab))
+        del memory, dy, old
