@@ -2,9 +2,11 @@
 //
 // Both are bound by HBM.  Measured: 32768 rows of 4096 out of an int8 table of
 // 32000 into bf16 53 us (306 MB); the gradient of 32768 x 4096 bf16 to a table of
-// 32000 in f32, tokens by 1/rank, 192 us (793 MB): sort 29, sums and zeros 152,
-// join 12; of 2048 x 1000 bf16 to a table of 4001 17 us (7, 6 and 4 on the
-// device); of 511 x 1000 f32 9 us in one launch.
+// 32000 in f32, tokens by 1/rank, 192 us (793 MB): sort 29, sums and zeros 138-151,
+// join 11; of 2048 x 1000 bf16 to a table of 4001 17 us (7, 6 and 4 on the
+// device); of 511 x 1000 f32 9 us in one launch, 7.4-8.7 of them on the device.
+// Narrow rows to a small table are bound by the sort, whose workgroups are the
+// ranges of the table: 65536 x 64 to 256 rows takes 79 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -207,7 +209,7 @@ __global__ __launch_bounds__(kSmallThreads) void small_kernel(const void *__rest
     const uint32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
     const uint64_t lo = (uint64_t)blockIdx.x * range;
     const uint32_t size = (uint32_t)min((uint64_t)range, vocab - lo);
-    // each wave a consecutive part of the tokens, up to 4 in a lane
+    // each wave a consecutive part of the tokens, up to 2 in a lane
     constexpr uint32_t kEach = kSmall / kSmallThreads;
     const uint32_t per = (n + kSmallThreads - 1) / kSmallThreads * kWave;
     uint32_t mine[kEach];
@@ -616,8 +618,12 @@ uint32_t block_of(uint64_t n, uint64_t slabs) { return n * slabs <= 32768 ? 8 : 
 uint64_t slabs_of(uint64_t dim) { return (dim + kSlab - 1) / kSlab; }
 
 // One launch or three: the one pays for few tokens of a small range each.
-// 4001 x 1000, 512 tokens: 9 us against 16; 32000 x 2048 (62 rows a
-// workgroup), 512 tokens by 1/rank: 82 us against 57.
+// 4001 x 1000, 512 tokens: 10 us against 17; 32000 x 2048 (62 rows a
+// workgroup), 512 tokens by 1/rank: 82 us against 57.  Above 512 tokens it
+// still pays where they are spread (1024 by 1/rank: 14 against 17 us), but not
+// where most are one (nine in ten: 576 24 against 17.5 us, 1024 44 against 18;
+// 512 22); 15000 x 1000 (14 rows a workgroup): 576 tokens by 1/rank 25 against
+// 23 us, 1024 35 against 23.
 constexpr uint64_t kSmallRange = 16;
 uint64_t small_range(uint64_t vocab, uint64_t slabs) { return std::max<uint64_t>(4, vocab * slabs / 2048); }
 bool is_small(uint64_t n, uint64_t vocab, uint64_t dim) {

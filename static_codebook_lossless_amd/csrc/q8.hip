@@ -9,9 +9,12 @@
 // lie end to end in whole groups count as one row and need no division.
 //
 // Measured at 4096 x 16384 bf16 (a device copy reaches 5.2 TB/s): store 33 us
-// (6.1 TB/s), with the histogram 49 us, load 30 us (6.8 TB/s), the backward
-// pass of gate and up in one tensor with h 115 us (5.9 TB/s).  Small calls
-// (32 x 2048) take 4.4 us on the device and 9 us on the host.
+// (6.1 TB/s), with the histogram 49 us, load 29 us (6.8 TB/s), the backward
+// pass of gate and up in one tensor with h 109 us on the device, 115 through
+// the binding (5.9 TB/s).  In f32: load of 4096 x 8192 27 us (6.2 TB/s; 38 us
+// alone, when no part of the output is in the memory-side cache), that
+// backward pass of 2048 x 16384 115 us (5.2 TB/s).  Small calls (store of 32 x
+// 2048) take 3.7 us on the device and 10 us through the binding.
 #include <algorithm>
 #include <type_traits>
 

@@ -7,15 +7,22 @@
 // every lane the consecutive t of one column that the matrix instruction
 // takes.
 //
-// Bound by the matrix cores at their sustained clock (large tiles): 4096 rows,
-// 11008 x 4096 from e4m3 and bf16 into f32 take 317-343 us (1.08-1.17 PFLOP/s);
-// the matrix instructions alone, without loads and LDS, take 305 us, as 688
-// tiles are 2.7 rounds of 256 CUs.  A library product of the same shape with x
-// already in bf16 takes 379 us.  int8 takes 494 us: its symbols need 4.5 vector
-// instructions each, e4m3's half a one.  Small tiles with a long t (32768 rows,
-// 320 x 1000, int8) take 51 us and 6 us to join their slices; there the vector
-// work, the LDS and the matrix cores each take a third of the time and overlap
-// only between the two waves of a SIMD.
+// Large tiles are bound by the matrix cores at the clock they hold: 4096 rows,
+// 11008 x 4096 from e4m3 and bf16 into f32 take 317-326 us (1.13-1.17 PFLOP/s;
+// under the profiler, of few passes, 333-354); the matrix instructions alone,
+// without loads and LDS, take 305 us, as 688 tiles are 2.7 rounds of 256 CUs.
+// A library product of the same shape with x already in bf16 takes 379 us.
+// int8 takes 500 us: its symbols need 4.5 vector instructions each, e4m3's half
+// a one, and the one wave of a SIMD issues them between its matrix
+// instructions (matrix cores busy 34% of the time, e4m3 59%).  11007 x 4095
+// takes 411 us: rows of odd alignment cost 37 of the 90 more, the tile at the
+// operands' end (accumulators through 476 bytes of scratch a lane) and the
+// guarded epilogue the others.
+// Small tiles with a long t (32768 rows, 320 x 1000) take 44 us from e4m3 and
+// 50 from int8, and 6 us to join their slices.  No unit is full there (matrix
+// cores 31 and 26%, LDS 40 and 34%, vector issue 16 and 44%): the two waves of
+// a SIMD stand 42% of their time at waits for loads, LDS and barriers, and the
+// 24 tiles read the operands 2.2 times (116 of 52 MiB).
 #include <algorithm>
 #include <type_traits>
 
@@ -228,8 +235,9 @@ __device__ __forceinline__ void interleave() {
     }
 }
 
-// Three phases as one where the pieces take much vector work (int8, terms of
-// f16 and f32): 8 vector instructions behind each of the 48 matrix instructions.
+// Three phases as one where the pieces take much vector work (int8): 8 vector
+// instructions behind each of the 48 matrix instructions.  As above, only for
+// the large tiles, which f16 and f32 gradients do not take.
 template <uint32_t M>
 __device__ __forceinline__ void interleave_three() {
     if constexpr (M == 16) {
@@ -440,6 +448,9 @@ __global__ __launch_bounds__(WN *WK *kWave, FN * FK == 16 ? 1 : 2) void wgrad_ke
         }
     }
 
+    // Accumulating tiles take the guarded way, one load and store after the
+    // other: 4096 rows to 11008 x 4096 638 us against 321, 2048 to 4096 x 4096
+    // 136 against 67.
     const bool inside = n0 + BN <= s.n && k0 + BK <= s.k && !add;
     auto write = [&](auto o) {
         typedef typename Plain<decltype(o)::value>::type T;
@@ -537,8 +548,10 @@ __global__ __launch_bounds__(kThreads) void join_kernel(const float *__restrict_
 // large tiles and 81 in small ones, to 4096 x 2816 (176 large tiles) 54 and 59,
 // to 2048 x 4096 (128 large tiles) 51 and 41.  Fewer small tiles than CUs share
 // t in slices of at least 8 LDS tiles: 512 x 512 of 8192 rows takes 18 us so
-// and 22 us in slices of 4, 512 x 512 of 512 rows 12 and 17 us.  f16 and f32
-// gradients, of twice and three times the products, keep to the small tiles.
+// and 22 us in slices of 4, of 512 rows 12 and 16; 64 x 64 of 65536 rows 43 us,
+// in slices of 4 62 us, of 2 104 us (of 16384 rows 20, 20 and 30); 32 x 1024 of
+// 65536 rows 34 us in all three.  f16 and f32 gradients, of twice and three
+// times the products, keep to the small tiles.
 uint64_t tiles_of(uint64_t n, uint64_t k, uint32_t side) { return ((n + side - 1) / side) * ((k + side - 1) / side); }
 
 struct Plan {
