@@ -482,6 +482,134 @@ pc_status pc_embed_backward(const void *d_dy, int dy_dtype, size_t ld_dy, const 
                             int grad_dtype, size_t ld_grad, int accumulate, void *d_ws, size_t ws_bytes,
                             void *stream);
 
+/* ------------------------------------------------------------------------
+ * What a step does between its products: dropout, the norm with the
+ * residual's addition and an output in 8 bits, and log probabilities
+ * ------------------------------------------------------------------------ */
+
+/*
+ * A dropout mask.  It is stored nowhere: whether element (r, c) of a tensor
+ * is dropped follows from its place, the seed and the offset alone, so a
+ * backward pass makes the same mask again.
+ *   Numbers: Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random
+ *   numbers: as easy as 1, 2, 3", 2011) with the counter (c / 8, r, low word,
+ *   high word of the offset) and the seed's low and high word as the key.  Of
+ *   its four words, column c takes the low (c even) or high (c odd) 16 bits of
+ *   word (c mod 8) / 2; the element is dropped, whatever it holds, where they
+ *   are below T = 65536 p rounded to a whole number (ties to even).  The
+ *   others are multiplied by 65536 / (65536 - T).
+ *   p         0 (nothing is dropped) to 1 (everything is).
+ *   d_random  NULL, or two u64 in device memory (8-byte aligned): the seed, in
+ *             place of `seed`, and a number added to `offset` modulo 2^64.  A
+ *             captured graph reads them anew at each replay.
+ * Calls that shall not share a mask differ in seed or offset.  The struct is host memory, read during the call.
+ */
+typedef struct pc_mask {
+    double p;
+    uint64_t seed, offset;
+    const uint64_t *d_random;
+} pc_mask;
+
+/* out = mask(x): rows x cols of one dtype, each with its row distance; d_out may be d_x (same ld).  cols is below 2^31. */
+pc_status pc_dropout(const void *d_x, int dtype, size_t rows, size_t cols, size_t ldx, const pc_mask *mask,
+                     void *d_out, size_t ld_out, void *stream);
+
+/*
+ * Root-mean-square norm of a residual block's input, stored in 8 bits:
+ *   h = res + mask(x), rounded to sum_dtype
+ *   rstd = (mean of h^2 over the row + eps)^-1/2
+ *   y = h rstd weight
+ *   d_x      rows x cols of dtype, row distance ldx.
+ *   d_res    NULL (no residual: then sum_dtype is dtype), or rows x cols of sum_dtype: dtype or PC_F32.
+ *   mask     NULL, or the dropout of x.
+ *   d_weight NULL (1), or cols numbers of weight_dtype.
+ *   eps      positive and finite.
+ *   d_sum    NULL, or receives h; may be d_res, or d_x where the types agree (same ld).  NULL without d_res and mask (h is x).
+ *   d_sym, d_scale  NULL, or receive y as pc_q8_store would store it, dense;
+ *            d_counts as there (NULL without d_sym).  y goes into the stored
+ *            form from 32 bits, without an earlier rounding.
+ *   d_y      NULL, or receives y rounded to y_dtype; where y_stored, the stored
+ *            values in its place, as pc_q8_load gives them (needs d_sym).
+ *   d_rstd   NULL, or receives rows f32.
+ * Squares are summed in 64 bits.  A row that holds an infinity has rstd 0, one
+ * that holds NaN has rstd NaN.  cols is below 2^31.
+ */
+pc_status pc_rmsnorm_store(const void *d_x, int dtype, size_t rows, size_t cols, size_t ldx, const void *d_res,
+                           int sum_dtype, size_t ld_res, const pc_mask *mask, const void *d_weight, int weight_dtype,
+                           float eps, void *d_sum, size_t ld_sum, int format, uint8_t *d_sym, uint8_t *d_scale,
+                           uint64_t *d_counts, void *d_y, int y_dtype, size_t ld_y, int y_stored, float *d_rstd,
+                           void *stream);
+
+/*
+ * Backward pass of pc_rmsnorm_store.  With n = h rstd and g = dy weight:
+ *   d = rstd (g - n mean(g n)) + dsum
+ *   d_res = d,  d_x = mask(d),  d_weight = sum over the rows of dy n  (+ d_weight where accumulate)
+ *   d_dy     rows x cols of dtype, the gradient of y.
+ *   d_sum    h, rows x cols of sum_dtype (dtype or PC_F32); or NULL, and
+ *   stored_sum  h as it was stored, in its place.
+ *   d_rstd   rows f32, as the forward pass gave them.
+ *   d_dsum   NULL, or the gradient that reaches h on the residual's way, of sum_dtype.
+ *   mask     NULL, or the forward pass's.
+ *   d_dres   NULL, or receives d in sum_dtype; may be d_dsum (same ld).
+ *   d_dx     NULL, or receives mask(d) in dtype; may be d_dy (same ld).
+ *   d_dweight  NULL, or receives cols numbers of dweight_dtype; each is summed in 32 bits in an order that
+ *            depends on the sizes alone.
+ *   d_ws, ws_bytes  scratch of pc_rmsnorm_backward_workspace_bytes, 16-byte
+ *            aligned; needed where d_dweight is given, and rows.
+ * rows == 0: d_weight = 0, or stays where accumulate.
+ */
+size_t pc_rmsnorm_backward_workspace_bytes(size_t rows, size_t cols);
+pc_status pc_rmsnorm_backward(const void *d_dy, int dtype, size_t rows, size_t cols, size_t ld_dy, const void *d_sum,
+                              int sum_dtype, size_t ld_sum, const pc_q8 *stored_sum, const void *d_weight,
+                              int weight_dtype, const float *d_rstd, const void *d_dsum, size_t ld_dsum,
+                              const pc_mask *mask, void *d_dres, size_t ld_dres, void *d_dx, size_t ld_dx,
+                              void *d_dweight, int dweight_dtype, int accumulate, void *d_ws, size_t ws_bytes,
+                              void *stream);
+
+/*
+ * Log probabilities of rows of logits.  With z = scale x:
+ *   logp[j] = z[token[j]] - ln sum exp z,   entropy = - sum p ln p,  p = exp(logp)
+ *   d_logits  rows x vocab, row distance ld.  -infinity marks a token that cannot be chosen.
+ *   scale     2^-64 to 2^64: the inverse temperature.
+ *   d_tokens  rows x n_tokens (at most 64) of 4 or 8 bytes each, signed, dense: one or more for each row.
+ *   d_logp    rows x n_tokens f32 (NULL where n_tokens is 0).  A token equal to `padding` or outside [0, vocab) gets 0.
+ *   top       0 to 64, at most vocab: the largest logits of each row,
+ *             in descending order, equal ones by their index (NaN counts as
+ *             -infinity): d_top_index rows x top i64, d_top_logp f32.
+ *   d_stats   NULL, or rows x 4 f32 for the backward pass and the caller: the
+ *             row's largest logit, ln sum exp(z - scale largest), the entropy, and ln sum exp z.
+ *   d_status  NULL, or one u32 that the caller has zeroed: a token outside
+ *             [0, vocab) other than `padding` sets it to PC_ERR_INVALID_ARG.
+ *   d_ws, ws_bytes  scratch of pc_logprobs_workspace_bytes (which may be 0,
+ *             then d_ws may be NULL), 16-byte aligned.
+ * A row that is -infinity throughout has nothing to choose: log probabilities
+ * -infinity, entropy 0.  A row that holds NaN or +infinity: NaN.
+ * PC_ERR_UNSUPPORTED: more than 64 tokens or alternatives, and rows x
+ * ceil(vocab / 4096) of 2^31 and more.
+ */
+size_t pc_logprobs_workspace_bytes(size_t rows, size_t vocab, size_t top, int dtype);
+pc_status pc_logprobs(const void *d_logits, int dtype, size_t rows, size_t vocab, size_t ld, float scale,
+                      const void *d_tokens, int token_bytes, size_t n_tokens, int64_t padding, float *d_logp,
+                      size_t top, int64_t *d_top_index, float *d_top_logp, float *d_stats, uint32_t *d_status,
+                      void *d_ws, size_t ws_bytes, void *stream);
+
+/*
+ * Gradient of the logits, from those of the log probabilities and of the entropy:
+ *   dlogits[v] = scale (sum over j with token[j] == v of dlogp[j]
+ *                       - p[v] (sum over j of dlogp[j] + dentropy (ln p[v] + entropy)))
+ *   d_logits, scale, d_tokens, padding  as in the forward pass; d_stats what it gave.
+ *   d_dlogp   rows x n_tokens f32 (NULL where n_tokens is 0).  Of a token
+ *             equal to `padding` or outside the vocabulary it is not used.
+ *   d_dentropy  NULL, or rows f32.
+ *   d_dlogits rows x vocab of the logits' dtype; may be d_logits (same ld).
+ * Rows whose given gradients are all 0 get zeros, whatever their logits; so do
+ * rows that are -infinity throughout.
+ */
+pc_status pc_logprobs_backward(const void *d_logits, int dtype, size_t rows, size_t vocab, size_t ld, float scale,
+                               const float *d_stats, const void *d_tokens, int token_bytes, size_t n_tokens,
+                               int64_t padding, const float *d_dlogp, const float *d_dentropy, void *d_dlogits,
+                               size_t ld_out, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

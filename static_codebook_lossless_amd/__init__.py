@@ -17,3 +17,7 @@ from .q8 import (  # noqa: F401,E402
     pc_q8_store, pc_q8_weight_grad, pc_q8_weight_grad_workspace_bytes,
 )
 from .refresh import CodebookRefresh  # noqa: F401,E402
+from .step import (  # noqa: F401,E402
+    DropoutMask, LogProbs, RmsNorm, RmsNormGrads, pc_dropout, pc_logprobs, pc_logprobs_backward,
+    pc_logprobs_workspace_bytes, pc_rmsnorm_backward, pc_rmsnorm_backward_workspace_bytes, pc_rmsnorm_store,
+)

@@ -30,6 +30,8 @@ EXPORTS = [
     "pc_traffic_probe",
     "pc_q8_store", "pc_q8_load", "pc_q8_glu_backward", "pc_q8_weight_grad_workspace_bytes", "pc_q8_weight_grad",
     "pc_embed", "pc_embed_q8", "pc_embed_backward_workspace_bytes", "pc_embed_backward",
+    "pc_dropout", "pc_rmsnorm_store", "pc_rmsnorm_backward_workspace_bytes", "pc_rmsnorm_backward",
+    "pc_logprobs_workspace_bytes", "pc_logprobs", "pc_logprobs_backward",
 ]
 
 
@@ -43,6 +45,11 @@ class StoredArg(C.Structure):
     """The header's pc_q8: a stored tensor as an argument."""
     _fields_ = [("sym", C.c_void_p), ("scale", C.c_void_p), ("rows", C.c_uint64), ("cols", C.c_uint64),
                 ("ld_sym", C.c_uint64), ("ld_scale", C.c_uint64), ("format", C.c_int32), ("reserved", C.c_int32)]
+
+
+class MaskArg(C.Structure):
+    """The header's pc_mask: a dropout mask as an argument."""
+    _fields_ = [("p", C.c_double), ("seed", C.c_uint64), ("offset", C.c_uint64), ("d_random", C.c_void_p)]
 
 
 def _load():
@@ -81,11 +88,23 @@ def _load():
     lib.pc_embed_backward_workspace_bytes.argtypes = [sz, sz, sz]
     lib.pc_embed_backward_workspace_bytes.restype = sz
     lib.pc_embed_backward.argtypes = [p, i, sz, p, i, sz, sz, sz, i64, f32, p, i, sz, i, p, sz, p]
+    mask = C.POINTER(MaskArg)
+    lib.pc_dropout.argtypes = [p, i, sz, sz, sz, mask, p, sz, p]
+    lib.pc_rmsnorm_store.argtypes = [p, i, sz, sz, sz, p, i, sz, mask, p, i, f32, p, sz, i, p, p, p, p, i, sz, i, p, p]
+    lib.pc_rmsnorm_backward_workspace_bytes.argtypes = [sz, sz]
+    lib.pc_rmsnorm_backward_workspace_bytes.restype = sz
+    lib.pc_rmsnorm_backward.argtypes = [p, i, sz, sz, sz, p, i, sz, q8, p, i, p, p, sz, mask, p, sz, p, sz, p, i, i, p,
+                                        sz, p]
+    lib.pc_logprobs_workspace_bytes.argtypes = [sz, sz, sz, i]
+    lib.pc_logprobs_workspace_bytes.restype = sz
+    lib.pc_logprobs.argtypes = [p, i, sz, sz, sz, f32, p, i, sz, i64, p, sz, p, p, p, p, p, sz, p]
+    lib.pc_logprobs_backward.argtypes = [p, i, sz, sz, sz, f32, p, p, i, sz, i64, p, p, p, sz, p]
     for f in ("pc_codebook_build", "pc_codebook_validate", "pc_qlc_optimal_bits", "pc_codebook_fit",
               "pc_shard_code_lengths", "pc_encode", "pc_encode_noalloc",
               "pc_decode", "pc_decode_qlc", "pc_histogram", "pc_traffic_probe",
               "pc_q8_store", "pc_q8_load", "pc_q8_glu_backward", "pc_q8_weight_grad",
-              "pc_embed", "pc_embed_q8", "pc_embed_backward"):
+              "pc_embed", "pc_embed_q8", "pc_embed_backward",
+              "pc_dropout", "pc_rmsnorm_store", "pc_rmsnorm_backward", "pc_logprobs", "pc_logprobs_backward"):
         getattr(lib, f).restype = i
     return lib
 

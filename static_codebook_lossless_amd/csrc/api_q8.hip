@@ -1,42 +1,9 @@
 // C-ABI entry points of the stored-tensor and embedding operators: argument
 // checks and HIP error mapping.  The kernels live in q8.hip, wgrad.hip and
 // embed.hip.
-#include "pc_internal.h"
+#include "checks.h"
 
-namespace {
-
-// A launch has fewer than 2^24 workgroups of 256 lanes; the smallest tile is
-// 512 units of 8 columns.
-constexpr uint64_t kMaxGroups = (1ull << 24) - 1;
-constexpr uint64_t kMaxWidth = 1ull << 31;
-constexpr uint64_t kMaxDistance = 1ull << 24;  // weight gradient: offsets inside a tile of 64 rows stay below 2^32 bytes
-constexpr uint64_t kMaxElements = 1ull << 47;  // beyond any memory; keeps sizes below 64 bits
-
-bool is_dtype(int d) { return d == PC_F32 || d == PC_F16 || d == PC_BF16; }
-bool is_format(int f) { return f == PC_Q8_E4M3 || f == PC_Q8_INT8; }
-
-// rows x cols elements of a dtype at p, row distance ld.
-bool plain_ok(const void *p, int dtype, size_t cols, size_t ld) {
-    return p && ld >= cols && (reinterpret_cast<uintptr_t>(p) & (dtype == PC_F32 ? 3 : 1)) == 0;
-}
-
-bool stored_ok(const pc_q8 *q) {
-    return q->sym && q->scale && q->ld_sym >= q->cols && q->ld_scale >= (q->cols + 31) / 32;
-}
-
-bool size_ok(uint64_t rows, uint64_t cols) {
-    if (cols >= kMaxWidth) return false;
-    if (cols == 0 || rows == 0) return true;
-    const uint64_t padded = (cols + 31) / 32 * 32;
-    return rows <= kMaxElements / padded && (rows * (padded / 8) + 511) / 512 <= kMaxGroups;
-}
-
-// The distance from a tensor's first to its last row fits 63 bits in bytes.
-bool span_ok(uint64_t rows, uint64_t ld) { return rows == 0 || ld <= (1ull << 60) / rows; }
-
-pc_status map_hip(hipError_t e) { return e == hipSuccess ? PC_OK : PC_ERR_HIP; }
-
-}  // namespace
+using namespace pc::checks;
 
 extern "C" {
 

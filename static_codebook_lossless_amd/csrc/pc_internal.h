@@ -134,4 +134,60 @@ hipError_t launch_embed_backward(const void *dy, int dtype, uint64_t ld_dy, cons
                                  uint32_t n, uint64_t dim, uint64_t vocab, int64_t padding, float scale, void *grad,
                                  int grad_dtype, uint64_t ld_grad, bool accumulate, void *ws, hipStream_t stream);
 
+// Arguments of the norm's entries; dtypes are pc_dtypes, NULL what is not wanted.
+struct RmsNorm {
+    const void *x, *res, *weight;
+    void *sum, *y;
+    uint8_t *sym, *scale;
+    uint64_t *counts;
+    float *rstd;
+    const pc_mask *mask;
+    uint64_t rows, cols, ldx, ld_res, ld_sum, ld_y;
+    int dtype, sum_dtype, weight_dtype, y_dtype, format, y_stored;
+    float eps;
+};
+hipError_t launch_rmsnorm_store(const RmsNorm &c, hipStream_t stream);
+
+struct RmsNormGrad {
+    const void *dy, *sum, *d_sum, *weight;
+    const pc_q8 *stored;  // in place of sum
+    const float *rstd;
+    void *d_res, *d_x, *d_weight, *ws;
+    const pc_mask *mask;
+    uint64_t rows, cols, ld_dy, ld_sum, ld_d_sum, ld_d_res, ld_d_x;
+    int dtype, sum_dtype, weight_dtype, d_weight_dtype, accumulate;
+};
+uint64_t rmsnorm_backward_workspace(uint64_t rows, uint64_t cols);
+hipError_t launch_rmsnorm_backward(const RmsNormGrad &c, hipStream_t stream);
+
+hipError_t launch_dropout(const void *x, int dtype, uint64_t rows, uint64_t cols, uint64_t ldx, const pc_mask *mask,
+                          void *out, uint64_t ld_out, hipStream_t stream);
+
+struct LogProbs {
+    const void *logits, *tokens;
+    float *logp, *top_logp, *stats;
+    int64_t *top_index;
+    uint32_t *status;
+    void *ws;
+    uint64_t rows, vocab, ld;
+    int64_t padding;
+    uint32_t n_tokens, top;
+    int dtype, token_bytes;
+    float scale;
+};
+uint64_t logprobs_workspace(uint64_t rows, uint64_t vocab, uint32_t top, int dtype);
+hipError_t launch_logprobs(const LogProbs &c, hipStream_t stream);
+
+struct LogProbsGrad {
+    const void *logits, *tokens;
+    const float *stats, *d_logp, *d_entropy;
+    void *d_logits;
+    uint64_t rows, vocab, ld, ld_out;
+    int64_t padding;
+    uint32_t n_tokens;
+    int dtype, token_bytes;
+    float scale;
+};
+hipError_t launch_logprobs_backward(const LogProbsGrad &c, hipStream_t stream);
+
 }  // namespace pc

@@ -193,6 +193,80 @@ __device__ __forceinline__ void unit_values(u32x2 w, float scale, float v[8]) {
     }
 }
 
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+    v = max(v, dpp_u32<0xB1>(v));  // neighbour in the pair
+    return max(v, dpp_u32<0x4E>(v));  // the other pair
+}
+
+// The scale code for the largest magnitude (as bits) of a group.  With
+// top = m 2^e, 1 <= m < 2:  top <= M 2^k  needs k = e - 8, one more where
+// m > 1.75 (M = 448), or k = e - 6, one more where m > 127/64 (M = 127).
+template <int FMT>
+__device__ __forceinline__ uint32_t code_for(uint32_t top) {
+    const uint32_t e = top >> 23, m = top & 0x7FFFFFu;
+    const int code = FMT == PC_Q8_E4M3 ? (int)e - 8 + (m > 0x600000u) : (int)e - 6 + (m > 0x7E0000u);
+    return (uint32_t)max(code, (int)kMinCode);
+}
+
+template <int FMT>
+__device__ __forceinline__ u32x2 to_symbols(const float v[8], float inv) {
+    u32x2 w;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float *x = v + 4 * k;
+        if constexpr (FMT == PC_Q8_E4M3) {
+            int p = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * inv, x[1] * inv, 0, false);
+            w[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[2] * inv, x[3] * inv, p, true);
+        } else {
+            // adding 3 * 2^22 rounds to a whole number, ties to even, whose
+            // two's complement is then in the low bits
+            uint32_t r[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] = as_u32(x[i] * inv + 12582912.0f) & 0xFFu;
+            w[k] = r[0] | r[1] << 8 | r[2] << 16 | r[3] << 24;
+        }
+    }
+    return w;
+}
+
+template <int FMT>
+__device__ __forceinline__ u32x2 with_nan(u32x2 w, uint32_t bad) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (bad >> i & 1) {
+            const uint32_t s = 8 * (i % 4);
+            w[i / 4] = (w[i / 4] & ~(0xFFu << s)) | (uint32_t)(FMT == PC_Q8_E4M3 ? 0x7F : 0x80) << s;
+        }
+    return w;
+}
+
+// The symbols of the lane's 8 values and their group's scale code.  The four
+// lanes that hold a group take part together; v is changed where it holds
+// infinities and NaN, which take no part in the scale.
+template <int FMT>
+__device__ __forceinline__ u32x2 to_stored(float v[8], uint32_t &code) {
+    uint32_t top = 0, bad = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = max(top, as_u32(v[i]) & 0x7FFFFFFFu);
+    if (top >= 0x7F800000u) {
+        top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t a = as_u32(v[i]) & 0x7FFFFFFFu;
+            if (a >= 0x7F800000u) {
+                bad |= 1u << i;
+                v[i] = 0.0f;
+            } else {
+                top = max(top, a);
+            }
+        }
+    }
+    code = code_for<FMT>(quad_max(top));
+    u32x2 w = to_symbols<FMT>(v, as_f32((254 - code) << 23));
+    if (bad) w = with_nan<FMT>(w, bad);
+    return w;
+}
+
 // Division of t < 2^31 by a number fixed before the launch.
 struct Divider {
     uint32_t d, magic, shift;
