@@ -585,7 +585,7 @@ pc_status pc_rmsnorm_backward(const void *d_dy, int dtype, size_t rows, size_t c
  * A row that is -infinity throughout has nothing to choose: log probabilities
  * -infinity, entropy 0.  A row that holds NaN or +infinity: NaN.
  * PC_ERR_UNSUPPORTED: more than 64 tokens or alternatives, and rows x
- * ceil(vocab / 4096) of 2^31 and more.
+ * ceil(vocab / 1024) of 2^31 and more.
  */
 size_t pc_logprobs_workspace_bytes(size_t rows, size_t vocab, size_t top, int dtype);
 pc_status pc_logprobs(const void *d_logits, int dtype, size_t rows, size_t vocab, size_t ld, float scale,

@@ -29,7 +29,7 @@ bool tokens_ok(const void *tokens, int token_bytes, size_t n) {
 
 // Rows of logits: the launches count them, and their stretches, in 32 bits.
 bool logits_size_ok(uint64_t rows, uint64_t vocab) {
-    return size_ok(rows, vocab) && rows * ((vocab + 4095) / 4096) < (1ull << 31);
+    return size_ok(rows, vocab) && rows * ((vocab + 1023) / 1024) < (1ull << 31);
 }
 
 }  // namespace

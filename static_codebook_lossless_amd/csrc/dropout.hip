@@ -1,7 +1,5 @@
 // Dropout: out = mask(x), the mask made from a counter in the kernel.  Its
 // backward pass is the same call on the gradient.
-#include <algorithm>
-
 #include "random.h"
 
 namespace pc {

@@ -22,17 +22,17 @@ constexpr float kGone = -1000.0f;  // 2^-1000 is 0 in 32 bits, and 0 times -1000
 
 template <int DT> constexpr uint32_t kPer = DT == PC_F32 ? 4 : 8;  // elements of 16 bytes
 
-template <int DT>
+template <int DT, bool STREAM>
 __device__ __forceinline__ u32x4 load_vec(const typename Plain<DT>::type *p, uint32_t n) {
     if constexpr (DT == PC_F32) {
-        if (n == 4) return *reinterpret_cast<const u32x4_any4 *>(p);
+        if (n == 4) return get<u32x4, 4, STREAM>(p);
         u32x4 r = {0, 0, 0, 0};
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i)
             if (i < n) r[i] = as_u32(p[i]);
         return r;
     } else {
-        return load_raw<DT>(p, n).w[0];
+        return load_raw<DT, STREAM>(p, n).w[0];
     }
 }
 
@@ -73,42 +73,61 @@ __device__ __forceinline__ float from_lane(float v, uint32_t lane) { return as_f
 // running maximum and sums
 // ---------------------------------------------------------------------------
 
-// Of some elements: their largest m (at least the lowest finite number), and
-// with u = (x - m) scale log2(e), the sums of 2^u and of 2^u u.  NaN and
-// +infinity make s NaN; s is 0 where every element is -infinity.
-struct Soft { float m, s, t; };
+// Of some elements: the largest one m (-infinity for none), r = m c with
+// c = scale log2(e), rounded and held among the finite numbers, and with
+// u = x c - r the sums of 2^u and of 2^u u.  Everything is relative to the
+// rounded r, so an exponent takes one multiply-add, and what r lost is put
+// right once at the end.  NaN makes s NaN.
+struct Soft { float m, r, s, t; };
 
-__device__ __forceinline__ Soft nothing() { return {kLowest, 0.0f, 0.0f}; }
+__device__ __forceinline__ float held(float v) { return fminf(fmaxf(v, kLowest), -kLowest); }
 
-// fmaxf takes the other operand where one is NaN
-__device__ __forceinline__ Soft moved(Soft a, float m, float c) {
-    const float u = fmaxf((a.m - m) * c, kGone), f = __builtin_amdgcn_exp2f(u);
-    return {m, a.s * f, f * (a.t + u * a.s)};
+__device__ __forceinline__ Soft nothing() { return {-__builtin_inff(), kLowest, 0.0f, 0.0f}; }
+
+// The same sums for another, larger r (fmaxf takes the other operand where one is NaN).
+__device__ __forceinline__ Soft moved(Soft a, float m, float r) {
+    const float u = fmaxf(a.r - r, kGone), f = __builtin_amdgcn_exp2f(u);
+    return {m, r, a.s * f, f * (a.t + u * a.s)};
 }
 
-__device__ __forceinline__ Soft joined(Soft a, Soft b, float c) {
-    const float m = fmaxf(a.m, b.m);
-    a = moved(a, m, c);
-    b = moved(b, m, c);
-    return {m, a.s + b.s, a.t + b.t};
+// An r that was held stands for any m beyond it: only sums of one m go together.
+__device__ __forceinline__ Soft moved_exactly(Soft a, float m, float r) {
+    if (fabsf(r) == -kLowest && a.m != m) return {m, r, a.s != a.s ? a.s : 0.0f, 0.0f};
+    return moved(a, m, r);
 }
 
 template <int CTRL>
-__device__ __forceinline__ Soft dpp_soft(Soft v) {
-    return {as_f32(dpp_u32<CTRL>(as_u32(v.m))), as_f32(dpp_u32<CTRL>(as_u32(v.s))), as_f32(dpp_u32<CTRL>(as_u32(v.t)))};
+__device__ __forceinline__ float dpp_f32(float v) { return as_f32(dpp_u32<CTRL>(as_u32(v))); }
+
+// Sum and maximum over a wave, the same in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+    v += dpp_f32<0xB1>(v);   // the neighbour in the pair
+    v += dpp_f32<0x4E>(v);   // the other pair
+    v += dpp_f32<0x141>(v);  // the other half of 8
+    v += dpp_f32<0x140>(v);  // the other half of 16
+    return (from_lane(v, 0) + from_lane(v, 16)) + (from_lane(v, 32) + from_lane(v, 48));
 }
 
-__device__ __forceinline__ Soft soft_of(Soft v, uint32_t lane) {
-    return {from_lane(v.m, lane), from_lane(v.s, lane), from_lane(v.t, lane)};
+__device__ __forceinline__ float wave_max(float v) {
+    v = fmaxf(v, dpp_f32<0xB1>(v));
+    v = fmaxf(v, dpp_f32<0x4E>(v));
+    v = fmaxf(v, dpp_f32<0x141>(v));
+    v = fmaxf(v, dpp_f32<0x140>(v));
+    return fmaxf(fmaxf(from_lane(v, 0), from_lane(v, 16)), fmaxf(from_lane(v, 32), from_lane(v, 48)));
+}
+
+__device__ __forceinline__ Soft joined(Soft a, Soft b, float c) {
+    const float m = fmaxf(a.m, b.m), r = held(m * c);
+    a = moved_exactly(a, m, r);
+    b = moved_exactly(b, m, r);
+    return {m, r, a.s + b.s, a.t + b.t};
 }
 
 // All lanes' joined, the same in every lane.
 __device__ __forceinline__ Soft wave_soft(Soft v, float c) {
-    v = joined(v, dpp_soft<0xB1>(v), c);
-    v = joined(v, dpp_soft<0x4E>(v), c);
-    v = joined(v, dpp_soft<0x141>(v), c);
-    v = joined(v, dpp_soft<0x140>(v), c);
-    return joined(joined(soft_of(v, 0), soft_of(v, 16), c), joined(soft_of(v, 32), soft_of(v, 48), c), c);
+    const float m = wave_max(v.m);
+    v = moved_exactly(v, m, held(m * c));
+    return {m, v.r, wave_sum(v.s), wave_sum(v.t)};
 }
 
 // ---------------------------------------------------------------------------
@@ -122,64 +141,111 @@ __device__ __forceinline__ uint32_t key_of(float x) {
     return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 
-// The wave's 64 largest elements so far, one a lane in descending order, equal
-// ones by their index.
-struct Best { uint32_t key, index; };
+__device__ __forceinline__ float of_key(uint32_t k) { return as_f32(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 
-__device__ __forceinline__ uint64_t packed(Best b) { return (uint64_t)b.key << 32 | (b.key ? ~b.index : 0u); }
+// An element as one number: larger ones first, of equal ones that of the lower
+// index.  0 stands for no element.
+__device__ __forceinline__ uint64_t packed(uint32_t key, uint32_t index) {
+    return (uint64_t)key << 32 | (uint32_t)~index;
+}
 
-__device__ __forceinline__ Best unpacked(uint64_t p) { return {(uint32_t)(p >> 32), ~(uint32_t)p}; }
+__device__ __forceinline__ uint32_t index_of(uint64_t p) { return ~(uint32_t)p; }
 
-// An element whose index is larger than those of all equal ones in the list.
-__device__ __forceinline__ void insert(Best &b, uint32_t key, uint32_t index) {
+// The value of lane (lane ^ D).  Rows of 16 lanes by DPP; between them by the
+// swaps of odd with even rows, and of the halves, of two registers that hold
+// the same.
+template <uint32_t D>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t v) {
     const uint32_t lane = threadIdx.x % kWave;
-    const uint32_t place = (uint32_t)__popcll(__ballot(b.key >= key));
-    const uint32_t key_before = dpp_u32<0x138>(b.key), index_before = dpp_u32<0x138>(b.index);  // from the lane below
-    if (lane > place) {
-        b.key = key_before;
-        b.index = index_before;
-    } else if (lane == place) {
-        b.key = key;
-        b.index = index;
+    if constexpr (D == 1) return dpp_u32<0xB1>(v);
+    if constexpr (D == 2) return dpp_u32<0x4E>(v);
+    if constexpr (D == 4) return (uint32_t)__builtin_amdgcn_ds_swizzle((int)v, 0x101F);
+    if constexpr (D == 8) return dpp_u32<0x128>(v);
+    if constexpr (D == 15) return dpp_u32<0x140>(v);
+    if constexpr (D == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return lane & 16 ? r[0] : r[1];
+    }
+    if constexpr (D == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return lane & 32 ? r[0] : r[1];
     }
 }
 
-// Takes the elements v of every lane (the first n count, from index `first`
-// on) into the list, where they are larger than the `top`th one.
-template <int N>
-__device__ __forceinline__ void take(Best &b, uint32_t top, float largest, const float v[N], uint32_t n, uint32_t first) {
-    uint32_t least = from_lane(b.key, top - 1);
-    const uint32_t key = n ? key_of(largest) : 0;
-    uint64_t left = __ballot(key > least);
-    while (left) {
-        const uint32_t lane = (uint32_t)__builtin_ctzll(left);
-        const uint32_t count = from_lane(n, lane), index = from_lane(first, lane);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const uint32_t k = key_of(from_lane(v[i], lane));
-            if ((uint32_t)i < count && k > least) {
-                insert(b, k, index + i);
-                least = from_lane(b.key, top - 1);
-            }
-        }
-        left &= left - 1;
-        left &= __ballot(key > least);
-    }
+template <uint32_t D>
+__device__ __forceinline__ uint64_t lane_xor(uint64_t v) {
+    return (uint64_t)lane_xor<D>((uint32_t)(v >> 32)) << 32 | lane_xor<D>((uint32_t)v);
 }
 
-// The 64 largest of two lists: the larger of one list and the other one turned
-// round are they, and rise to one place and fall from it, or the reverse.
-__device__ __forceinline__ uint64_t merged(uint64_t a, uint64_t b) {
-    const uint32_t lane = threadIdx.x % kWave;
-    const uint64_t turned = __shfl(b, 63 - lane, 64);
+// One step of a bitonic network: lanes D apart exchange, the larger one goes
+// to the lane without D where `descends`.
+template <uint32_t D, class T>
+__device__ __forceinline__ void exchange(T &v, bool descends) {
+    const T o = lane_xor<D>(v);
+    const bool keep = ((threadIdx.x & D) == 0) == descends;
+    v = keep == (v > o) ? v : o;
+}
+
+// The last steps of a sort: a list that rises to one place and falls from it
+// (or the reverse, or either turned round its end) in descending order.
+template <class T>
+__device__ __forceinline__ void descend(T &v) {
+    exchange<32>(v, true), exchange<16>(v, true), exchange<8>(v, true), exchange<4>(v, true), exchange<2>(v, true),
+        exchange<1>(v, true);
+}
+
+// A lane's value each, in descending order.
+template <class T>
+__device__ __forceinline__ T sorted(T v) {
+    const uint32_t l = threadIdx.x;
+    exchange<1>(v, !(l & 2));
+    exchange<2>(v, !(l & 4)), exchange<1>(v, !(l & 4));
+    exchange<4>(v, !(l & 8)), exchange<2>(v, !(l & 8)), exchange<1>(v, !(l & 8));
+    exchange<8>(v, !(l & 16)), exchange<4>(v, !(l & 16)), exchange<2>(v, !(l & 16)), exchange<1>(v, !(l & 16));
+    exchange<16>(v, !(l & 32)), exchange<8>(v, !(l & 32)), exchange<4>(v, !(l & 32)), exchange<2>(v, !(l & 32)),
+        exchange<1>(v, !(l & 32));
+    descend(v);
+    return v;
+}
+
+// The 64 largest of two descending lists, descending: the larger ones of one
+// list and of the other one turned round.
+template <class T>
+__device__ __forceinline__ T merged(T a, T b) {
+    const T turned = lane_xor<32>(lane_xor<16>(lane_xor<15>(b)));
     a = a > turned ? a : turned;
-#pragma unroll
-    for (uint32_t d = 32; d; d >>= 1) {
-        const uint64_t o = __shfl_xor(a, d, 64);
-        const bool low = (lane & d) == 0;
-        a = low == (a > o) ? a : o;
-    }
+    descend(a);
     return a;
+}
+
+// A wave's largest elements so far, a lane each in descending order, and in
+// LDS those that may be among them: 64 of these together are sorted and merged.
+constexpr uint32_t kPool = 2 * kWave;
+
+struct Best {
+    uint64_t list, least, *pool;  // least: the `top`th of the list
+    uint32_t count;
+};
+
+__device__ __forceinline__ void wave_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ uint64_t lane_of(uint64_t v, uint32_t lane) {
+    return (uint64_t)from_lane((uint32_t)(v >> 32), lane) << 32 | from_lane((uint32_t)v, lane);
+}
+
+__device__ __forceinline__ void settle(Best &b, uint32_t top) {
+    const uint32_t lane = threadIdx.x % kWave;
+    wave_order();
+    const uint64_t v = sorted(lane < b.count ? b.pool[lane] : 0), rest = b.pool[kWave + lane];
+    wave_order();
+    b.pool[lane] = rest;
+    wave_order();
+    b.count = b.count > kWave ? b.count - kWave : 0;
+    b.list = b.least ? merged(b.list, v) : v;
+    b.least = lane_of(b.list, top - 1);
 }
 
 struct Args {
@@ -220,49 +286,134 @@ __device__ __forceinline__ void join_waves(Soft &soft, uint64_t &best, float c, 
     if (wave == 0) soft = wave_soft(lane < waves ? softs[lane] : nothing(), c);
 }
 
-// One wave writes a row's results.
-template <int DT, bool TOP>
-__device__ __forceinline__ void finish(const Args &a, uint64_t row, Soft soft, uint64_t best) {
-    typedef typename Plain<DT>::type T;
+// What a lane of the finishing wave needs for its token, loaded early.
+struct Picked {
+    float x;
+    bool inside, bad;
+};
+
+template <int DT>
+__device__ __forceinline__ Picked pick(const Args &a, uint64_t row) {
+    Picked p = {0.0f, false, false};
     const uint32_t lane = threadIdx.x % kWave;
-    const T *x = static_cast<const T *>(a.logits) + row * a.ld;
-    const bool empty = soft.s == 0.0f;
-    const float minus = -__builtin_inff();
-    const float log_sum = logf(soft.s);
-    auto logp_of = [&](float v) { return empty ? minus : (v - soft.m) * a.scale - log_sum; };
     if (lane < a.n_tokens) {
-        const uint64_t i = row * a.n_tokens + lane;
-        const int64_t t = token_at(a.tokens, a.token_bytes, i);
-        float logp = 0.0f;
-        if (t != a.padding) {
-            if (t >= 0 && t < (int64_t)a.vocab) logp = logp_of(widen(x[t]));
-            else if (a.status) *a.status = PC_ERR_INVALID_ARG;
-        }
-        a.logp[i] = logp;
+        const int64_t t = token_at(a.tokens, a.token_bytes, row * a.n_tokens + lane);
+        const bool in = t >= 0 && t < (int64_t)a.vocab;
+        p.inside = in && t != a.padding;
+        p.bad = !in && t != a.padding;
+        if (p.inside) p.x = widen((static_cast<const typename Plain<DT>::type *>(a.logits) + row * a.ld)[t]);
     }
+    return p;
+}
+
+// At most 0, which the last digits of a sum of 1 could pass; NaN stays.
+__device__ __forceinline__ float no_more_than_0(float v) { return v > 0.0f ? 0.0f : v; }
+
+// One wave writes a row's results.
+template <bool TOP>
+__device__ __forceinline__ void finish(const Args &a, uint64_t row, Soft soft, uint64_t best, Picked p) {
+    const uint32_t lane = threadIdx.x % kWave;
+    const float minus = -__builtin_inff();
+    const bool empty = soft.m == minus && soft.s == 0.0f;
+    // of m: what r lost; 0 where it was held.  +infinity leaves nothing to compare
+    const float lost = fabsf(soft.r) == -kLowest ? 0.0f : __builtin_fmaf(soft.m, a.scale * kLog2E, -soft.r);
+    const float bits = soft.m == -minus ? __builtin_nanf("") : log2f(soft.s);
+    const float log_sum = kLn2 * (bits - lost);
+    auto logp_of = [&](float v) { return empty ? minus : no_more_than_0((v - soft.m) * a.scale - log_sum); };
+    if (lane < a.n_tokens) a.logp[row * a.n_tokens + lane] = p.inside ? logp_of(p.x) : 0.0f;
+    if (p.bad && a.status) *a.status = PC_ERR_INVALID_ARG;
     if constexpr (TOP) {
         if (lane < a.top) {
-            const uint32_t index = unpacked(best).index;
-            a.top_index[row * a.top + lane] = index;
-            a.top_logp[row * a.top + lane] = logp_of(widen(x[index]));
+            a.top_index[row * a.top + lane] = index_of(best);
+            a.top_logp[row * a.top + lane] = logp_of(of_key((uint32_t)(best >> 32)));
         }
     }
     if (lane == 0 && a.stats) {
         float *s = a.stats + 4 * row;
-        s[0] = empty ? minus : soft.m;
-        s[1] = log_sum;
-        s[2] = empty ? 0.0f : log_sum - kLn2 * (soft.t / soft.s);
+        s[0] = soft.m;
+        s[1] = empty ? minus : log_sum;
+        s[2] = empty ? 0.0f : kLn2 * (bits - soft.t / soft.s);
         s[3] = empty ? minus : soft.m * a.scale + log_sum;
     }
 }
 
+constexpr uint32_t kRowThreads = 256;
+
+// The row's `top` largest elements, once every lane knows the largest of the
+// units it has read (its strip, every `threads`th unit from its own on).
+//
+// The `top`th largest of these lanes' largest is at most the `top`th of all
+// elements, and hardly less: the largest elements mostly lie in strips of their
+// own.  Strips whose largest is below it hold none of them; of the few others
+// the wave reads all units again, side by side, and takes what is not below the
+// bound.  So the pass over the row does nothing for the alternatives; a wave
+// that compares every element with the least it has kept so far does twice the
+// work (2048 x 32000 bf16, 20 of them: 66 us, without them 31).
+template <int DT>
+__device__ __forceinline__ uint64_t largest_elements(const Args &a, const typename Plain<DT>::type *x, uint32_t begin,
+                                                     uint32_t end, uint32_t key, uint32_t *keys, uint64_t *pool,
+                                                     uint8_t *strips) {
+    constexpr uint32_t N = kPer<DT>;
+    const uint32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave), threads = blockDim.x;
+    uint32_t best_keys = sorted(key);
+    if (threads > kWave) {
+        keys[threadIdx.x] = best_keys;
+        __syncthreads();
+        for (uint32_t w = 0; w < threads / kWave; ++w)
+            if (w != wave) best_keys = merged(best_keys, keys[w * kWave + lane]);
+    }
+    const uint32_t bound = max(1u, from_lane(best_keys, a.top - 1));  // 0: fewer lanes than that have read any
+    const uint64_t likely = __ballot(key >= bound);
+    const uint32_t count = (uint32_t)__builtin_popcountll(likely);
+    strips += wave * kWave;
+    if (key >= bound)
+        strips[__builtin_amdgcn_mbcnt_hi((uint32_t)(likely >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)likely, 0))] =
+            (uint8_t)lane;
+    wave_order();
+    Best b = {0, 0, pool + wave * kPool, 0};
+    // `wide` lanes to a strip (a power of two), 64 / wide strips at a time
+    const uint32_t length = (end - begin + threads - 1) / threads;
+    uint32_t log_wide = 0;
+    while (log_wide < 6 && (1u << log_wide) < length) ++log_wide;
+    const uint32_t wide = 1u << log_wide, together = kWave >> log_wide;
+    for (uint32_t s = 0; s < count; s += together) {
+        const uint32_t strip = s + (lane >> log_wide);
+        const uint32_t first = begin + wave * kWave + strips[min(strip, kWave - 1)];
+        for (uint32_t k0 = 0; k0 < length; k0 += wide) {
+            const uint32_t k = k0 + (lane & (wide - 1));
+            const uint32_t u = first + k * threads;
+            const uint32_t n = strip < count && k < length && u < end ? count_before(a.vocab, u * N, N) : 0;
+            float v[N];
+            widen_vec<DT>(load_vec<DT, false>(x + (uint64_t)u * N, n), v);
+#pragma unroll
+            for (uint32_t i = 0; i < N; ++i) {
+                const uint32_t vk = key_of(v[i]);
+                const uint64_t p = packed(vk, u * N + i);
+                const bool in = i < n && vk >= bound && p > b.least;
+                const uint64_t all = __ballot(in);
+                if (all) {
+                    if (in)
+                        b.pool[b.count + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32),
+                                                                   __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0))] = p;
+                    b.count += (uint32_t)__builtin_popcountll(all);
+                    if (b.count >= kWave) settle(b, a.top);
+                }
+            }
+        }
+    }
+    if (b.count) settle(b, a.top);
+    return b.list;
+}
+
 // A workgroup takes a row, or one of `splits` stretches of it.
-template <int DT, bool TOP>
-__global__ __launch_bounds__(kMaxThreads) void rows_kernel(Args a) {
+template <int DT, bool TOP, bool STREAM>
+__global__ __launch_bounds__(kRowThreads) void rows_kernel(Args a) {
     typedef typename Plain<DT>::type T;
     constexpr uint32_t N = kPer<DT>;
     __shared__ Soft softs[kMaxWaves];
-    __shared__ uint64_t lists[TOP ? kMaxThreads : 1];
+    __shared__ uint64_t lists[TOP ? kRowThreads : 1], pools[TOP ? kRowThreads / kWave * kPool : 1];
+    __shared__ uint32_t keys[TOP ? kRowThreads : 1];
+    __shared__ uint8_t strips[TOP ? kRowThreads : 1];
     const uint32_t tid = threadIdx.x, threads = blockDim.x, step = threads * kVecs;
     const float c = a.scale * kLog2E;
     const uint64_t total = a.rows * a.splits;
@@ -276,49 +427,79 @@ __global__ __launch_bounds__(kMaxThreads) void rows_kernel(Args a) {
             for (uint32_t j = 0; j < kVecs; ++j) {
                 const uint32_t u = base + j * threads + tid;
                 const uint32_t n = u < end ? count_before(a.vocab, u * N, N) : 0;
-                w[j] = load_vec<DT>(x + (uint64_t)u * N, n);
+                w[j] = load_vec<DT, STREAM>(x + (uint64_t)u * N, n);
             }
         };
+        Picked p = {};
+        if (a.splits == 1 && tid < kWave) p = pick<DT>(a, row);
         Soft soft = nothing();
-        Best best = {0, 0};
+        bool careful = false;
         u32x4 w[kVecs];
         load(begin, w);
         for (uint32_t base = begin; base < end; base += step) {
             u32x4 next[kVecs];
             load(base + step, next);
+            float v[kVecs][N], m = soft.m;
 #pragma unroll
             for (uint32_t j = 0; j < kVecs; ++j) {
                 const uint32_t u = base + j * threads + tid;
                 const uint32_t n = u < end ? count_before(a.vocab, u * N, N) : 0;
-                float v[N];
-                widen_vec<DT>(w[j], v);
+                widen_vec<DT>(w[j], v[j]);
                 if (n != N) {
 #pragma unroll
                     for (uint32_t i = 0; i < N; ++i)
-                        if (i >= n) v[i] = -__builtin_inff();
+                        if (i >= n) v[j][i] = -__builtin_inff();
                 }
-                float largest = v[0];
 #pragma unroll
-                for (uint32_t i = 1; i < N; ++i) largest = fmaxf(largest, v[i]);
-                if constexpr (TOP) take<N>(best, a.top, largest, v, n, u * N);
-                const float m = fmaxf(soft.m, largest);
-                soft = moved(soft, m, c);
-#pragma unroll
-                for (uint32_t i = 0; i < N; ++i) {
-                    const float y = (v[i] - m) * c, e = __builtin_amdgcn_exp2f(y);
-                    soft.s += e;
-                    soft.t += e * fmaxf(y, kGone);
-                }
+                for (uint32_t i = 0; i < N; ++i) m = fmaxf(m, v[j][i]);
             }
+            const float r = held(m * c);
+            soft = moved(soft, m, r);
+            auto sums = [&](auto mind, float &s, float &t) {
+                s = t = 0.0f;
+#pragma unroll
+                for (uint32_t j = 0; j < kVecs; ++j) {
+#pragma unroll
+                    for (uint32_t i = 0; i < N; ++i) {
+                        const float y = __builtin_fmaf(v[j][i], c, -r), e = __builtin_amdgcn_exp2f(y);
+                        s += e;
+                        t += e * (decltype(mind)::value ? fmaxf(y, kGone) : y);
+                    }
+                }
+            };
+            // -infinity makes t NaN (0 times it): a wave that has met one minds it from then on
+            float s, t;
+            if (!careful) {
+                sums(std::false_type(), s, t);
+                careful = __ballot(t != t) != 0;
+            }
+            if (careful) sums(std::true_type(), s, t);
+            soft.s += s;
+            soft.t += t;
 #pragma unroll
             for (uint32_t j = 0; j < kVecs; ++j) w[j] = next[j];
         }
+        const uint32_t key = begin + tid < end ? key_of(soft.m) : 0;
+        if (fabsf(soft.r) == -kLowest && fabsf(soft.m) <= -kLowest) {
+            // so large that neighbouring numbers differ by more than 2^64: those that equal m count
+            float same = 0.0f;
+            for (uint32_t u = begin + tid; u < end; u += threads) {
+                const uint32_t n = count_before(a.vocab, u * N, N);
+                float v[N];
+                widen_vec<DT>(load_vec<DT, false>(x + (uint64_t)u * N, n), v);
+#pragma unroll
+                for (uint32_t i = 0; i < N; ++i) same += i < n && v[i] == soft.m ? 1.0f : 0.0f;
+            }
+            if (soft.s == soft.s) soft.s = same;
+            soft.t = 0.0f;
+        }
         soft = wave_soft(soft, c);
-        uint64_t list = packed(best);
+        uint64_t list = 0;
+        if constexpr (TOP) list = largest_elements<DT>(a, x, begin, end, key, keys, pools, strips);
         join_waves<TOP>(soft, list, c, softs, lists);
         if (tid < kWave) {
             if (a.splits == 1) {
-                finish<DT, TOP>(a, row, soft, list);
+                finish<TOP>(a, row, soft, list, p);
             } else {
                 if (tid == 0) a.soft[id] = soft;
                 if (TOP && tid < a.top) a.best[id * a.top + tid] = list;
@@ -336,6 +517,8 @@ __global__ __launch_bounds__(kMaxThreads) void join_kernel(Args a) {
     const uint32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave), waves = blockDim.x / kWave;
     const float c = a.scale * kLog2E;
     const uint64_t row = blockIdx.x;
+    Picked p = {};
+    if (wave == 0) p = pick<DT>(a, row);
     Soft soft = nothing();
     uint64_t best = 0;
     for (uint32_t s = wave * kWave + lane; s < a.splits; s += blockDim.x)
@@ -346,7 +529,7 @@ __global__ __launch_bounds__(kMaxThreads) void join_kernel(Args a) {
             best = merged(best, lane < a.top ? a.best[(row * a.splits + s) * a.top + lane] : 0);
     }
     join_waves<TOP>(soft, best, c, softs, lists);
-    if (wave == 0) finish<DT, TOP>(a, row, soft, best);
+    if (wave == 0) finish<TOP>(a, row, soft, best, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -354,7 +537,8 @@ __global__ __launch_bounds__(kMaxThreads) void join_kernel(Args a) {
 // ---------------------------------------------------------------------------
 
 constexpr uint32_t kGradThreads = 256;
-constexpr uint32_t kGradUnits = kGradThreads * kVecs;
+constexpr uint32_t kGradVecs = 2;  // 4096 x 128000 bf16 with an entropy: one 420 us, two 367, four 368
+constexpr uint32_t kGradUnits = kGradThreads * kGradVecs;
 
 struct GradArgs {
     const void *logits, *tokens;
@@ -367,15 +551,7 @@ struct GradArgs {
     float scale;
 };
 
-__device__ __forceinline__ float wave_sum(float v) {
-    v += as_f32(dpp_u32<0xB1>(as_u32(v)));
-    v += as_f32(dpp_u32<0x4E>(as_u32(v)));
-    v += as_f32(dpp_u32<0x141>(as_u32(v)));
-    v += as_f32(dpp_u32<0x140>(as_u32(v)));
-    return (from_lane(v, 0) + from_lane(v, 16)) + (from_lane(v, 32) + from_lane(v, 48));
-}
-
-template <int DT, bool ENTROPY>
+template <int DT, bool ENTROPY, bool STREAM>
 __global__ __launch_bounds__(kGradThreads) void grad_kernel(GradArgs a) {
     typedef typename Plain<DT>::type T;
     constexpr uint32_t N = kPer<DT>;
@@ -384,13 +560,13 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(GradArgs a) {
         const uint32_t row = id / a.tiles, unit0 = (id - row * a.tiles) * kGradUnits;
         const T *x = static_cast<const T *>(a.logits) + row * a.ld;
         T *out = static_cast<T *>(a.out) + row * a.ld_out;
-        u32x4 w[kVecs];
-        uint32_t n[kVecs];
+        u32x4 w[kGradVecs];
+        uint32_t n[kGradVecs];
 #pragma unroll
-        for (uint32_t j = 0; j < kVecs; ++j) {
+        for (uint32_t j = 0; j < kGradVecs; ++j) {
             const uint32_t u = unit0 + j * kGradThreads + threadIdx.x;
             n[j] = count_before(a.vocab, u * N, N);
-            w[j] = load_vec<DT>(x + (uint64_t)u * N, n[j]);
+            w[j] = load_vec<DT, STREAM>(x + (uint64_t)u * N, n[j]);
         }
         // a token to a lane
         int64_t token = -1;
@@ -407,33 +583,43 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(GradArgs a) {
             entropy = a.stats[4 * (uint64_t)row + 2];
             de = a.d_entropy[row];
         }
-        const bool none = (__ballot(d != 0.0f) == 0 && de == 0.0f) || largest == -__builtin_inff();
-        const uint64_t inside =
-            __ballot(token >= (int64_t)unit0 * N && token < ((int64_t)unit0 + kGradUnits) * N && !none);
-        const uint32_t at = (uint32_t)token;
+        const bool none = (__ballot(d != 0.0f) == 0 && de == 0.0f) || (largest == -__builtin_inff() && log_sum == log_sum);
+        if (none) {
+            const float zeros[N] = {};
 #pragma unroll
-        for (uint32_t j = 0; j < kVecs; ++j) {
+            for (uint32_t j = 0; j < kGradVecs; ++j)
+                if (n[j]) store_vec<DT>(out + (uint64_t)(unit0 + j * kGradThreads + threadIdx.x) * N, n[j], zeros);
+            continue;
+        }
+        const uint64_t inside = __ballot(token >= (int64_t)unit0 * N && token < ((int64_t)unit0 + kGradUnits) * N);
+        const uint32_t at = (uint32_t)token;
+        // log2 p = x c - r - less:  r is largest c rounded, `less` has what that lost
+        const float c = a.scale * kLog2E, r = largest * c;
+        const bool huge = !(fabsf(r) < __builtin_inff());
+        const float less = __builtin_fmaf(log_sum, kLog2E, -__builtin_fmaf(largest, c, -r));
+        const float base = a.scale * (sum + de * entropy), slope = a.scale * de * kLn2;
+#pragma unroll
+        for (uint32_t j = 0; j < kGradVecs; ++j) {
+            if (!n[j]) continue;
             const uint32_t u = unit0 + j * kGradThreads + threadIdx.x;
             float v[N];
             widen_vec<DT>(w[j], v);
 #pragma unroll
             for (uint32_t i = 0; i < N; ++i) {
-                const float y = (v[i] - largest) * a.scale - log_sum;
-                const float p = __builtin_amdgcn_exp2f(y * kLog2E);
-                float g = sum;
-                if constexpr (ENTROPY) g += de * (fmaxf(y, kGone) + entropy);
-                v[i] = none ? 0.0f : -p * g;
+                float y = __builtin_fmaf(v[i], c, -r) - less;
+                if (huge) y = ((v[i] - largest) * a.scale - log_sum) * kLog2E;
+                const float p = __builtin_amdgcn_exp2f(y);
+                float g = base;
+                if constexpr (ENTROPY) g += slope * fmaxf(y, kGone);
+                v[i] = -p * g;
             }
             for (uint64_t left = inside; left; left &= left - 1) {
                 const uint32_t l = (uint32_t)__builtin_ctzll(left);
                 const uint32_t place = from_lane(at, l) - u * N;
-                const float add = from_lane(d, l);
+                const float add = a.scale * from_lane(d, l);
 #pragma unroll
                 for (uint32_t i = 0; i < N; ++i) v[i] += place == i ? add : 0.0f;
             }
-            if (!n[j]) continue;
-#pragma unroll
-            for (uint32_t i = 0; i < N; ++i) v[i] *= a.scale;
             store_vec<DT>(out + (uint64_t)u * N, n[j], v);
         }
     }
@@ -445,20 +631,31 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(GradArgs a) {
 
 uint32_t units_of(uint64_t vocab, int dtype) { return (uint32_t)((vocab + (dtype == PC_F32 ? 3 : 7)) / (dtype == PC_F32 ? 4 : 8)); }
 
+// Logits of so many bytes, which the memory-side cache does not hold, stream
+// past the caches (4096 x 128000 bf16: 192 us, streamed 168; 2048 x 32000: 29.6
+// and 28.1; 511 x 32001 f32, 62 MiB: 14.5 and 17.7).
+constexpr uint64_t kStreamBytes = 128ull << 20;
+
+bool streams(uint64_t rows, uint64_t vocab, int dtype) { return rows * vocab * (dtype == PC_F32 ? 4 : 2) >= kStreamBytes; }
+
 struct Plan { uint32_t threads, splits, per_split; };
 
+// A wave to a row where the rows fill the chip with waves and are short, or
+// hold no more than a wave's loads (8192 x 4000 bf16: 18 us, with four waves
+// 39; 2048 x 32000: 31 and 28).  Few rows are split, down to what a workgroup
+// loads at once, until there are two workgroups to a CU (1 x 128000: 6.8 us,
+// whole 20).
 Plan plan_rows(uint64_t rows, uint64_t vocab, int dtype) {
     Plan p;
     const uint32_t units = units_of(vocab, dtype);
-    p.threads = units <= 256 ? 64 : 256;
+    p.threads = units <= kRowThreads || (rows >= 4096 && units <= 4096) ? kWave : kRowThreads;
     p.splits = 1;
     p.per_split = units;
-    if (rows < 512 && units > 512) {
-        const uint32_t wanted = (uint32_t)std::min<uint64_t>(1024 / std::max<uint64_t>(rows, 1), units / 512);
-        if (wanted > 1) {
-            p.per_split = (units + wanted - 1) / wanted;
-            p.splits = (units + p.per_split - 1) / p.per_split;
-        }
+    const uint32_t least = kRowThreads * kVecs;
+    if (rows <= 256 && units >= 2 * least) {
+        const uint32_t wanted = (uint32_t)std::min<uint64_t>(512 / std::max<uint64_t>(rows, 1), units / least);
+        p.per_split = (units + wanted - 1) / wanted;
+        p.splits = (units + p.per_split - 1) / p.per_split;
     }
     return p;
 }
@@ -503,10 +700,13 @@ hipError_t launch_logprobs(const LogProbs &c, hipStream_t stream) {
         auto launch = [&](auto k, dim3 g, uint32_t threads) {
             hipLaunchKernelGGL(k, g, dim3(threads), 0, stream, a);
         };
-        if (c.top) launch(rows_kernel<DT, true>, grid, p.threads);
-        else launch(rows_kernel<DT, false>, grid, p.threads);
+        const bool stream_in = streams(c.rows, c.vocab, c.dtype);
+        if (c.top && stream_in) launch(rows_kernel<DT, true, true>, grid, p.threads);
+        else if (c.top) launch(rows_kernel<DT, true, false>, grid, p.threads);
+        else if (stream_in) launch(rows_kernel<DT, false, true>, grid, p.threads);
+        else launch(rows_kernel<DT, false, false>, grid, p.threads);
         if (p.splits > 1) {
-            const dim3 rows((uint32_t)c.rows);  // fewer than 512
+            const dim3 rows((uint32_t)c.rows);  // 256 at most
             if (c.top) launch(join_kernel<DT, true>, rows, kMaxThreads);
             else launch(join_kernel<DT, false>, rows, kWave);
         }
@@ -535,8 +735,11 @@ hipError_t launch_logprobs_backward(const LogProbsGrad &c, hipStream_t stream) {
     with_dtype(c.dtype, [&](auto d) {
         constexpr int DT = decltype(d)::value;
         auto launch = [&](auto k) { hipLaunchKernelGGL(k, grid, dim3(kGradThreads), 0, stream, a); };
-        if (c.d_entropy) launch(grad_kernel<DT, true>);
-        else launch(grad_kernel<DT, false>);
+        const bool stream_in = streams(c.rows, c.vocab, c.dtype);
+        if (c.d_entropy && stream_in) launch(grad_kernel<DT, true, true>);
+        else if (c.d_entropy) launch(grad_kernel<DT, true, false>);
+        else if (stream_in) launch(grad_kernel<DT, false, true>);
+        else launch(grad_kernel<DT, false, false>);
     });
     return hipGetLastError();
 }

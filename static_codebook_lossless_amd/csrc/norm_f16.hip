@@ -1,0 +1,16 @@
+// The norm's kernels for x in f16 and a sum in f16.
+#include "norm_kernels.h"
+
+namespace pc {
+
+template <>
+hipError_t norm_forward<PC_F16, PC_F16>(const NormArgs &a, const NormPlan &p, hipStream_t stream) {
+    return launch_norm<PC_F16, PC_F16>(a, p, stream);
+}
+
+template <>
+hipError_t norm_backward<PC_F16, PC_F16>(const GradArgs &a, const GradPlan &p, hipStream_t stream) {
+    return launch_norm_grad<PC_F16, PC_F16>(a, p, stream);
+}
+
+}  // namespace pc

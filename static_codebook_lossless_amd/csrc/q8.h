@@ -47,18 +47,27 @@ __device__ __forceinline__ uint32_t count_before(T end, T at, uint32_t most) {
     return left < most ? (uint32_t)left : most;
 }
 
+// A vector load from an address of a smaller alignment; STREAM: the caches
+// need not keep it.
+template <class V, uint32_t ALIGN, bool STREAM>
+__device__ __forceinline__ V get(const void *p) {
+    typedef V any __attribute__((aligned(ALIGN)));
+    if constexpr (STREAM) return __builtin_nontemporal_load(static_cast<const any *>(p));
+    else return *static_cast<const any *>(p);
+}
+
 // n (0..8) elements as loaded; the others 0.
 template <int DT> struct RawUnit { u32x4 w[DT == PC_F32 ? 2 : 1]; };
 
-template <int DT>
+template <int DT, bool STREAM = false>
 __device__ __forceinline__ RawUnit<DT> load_raw(const typename Plain<DT>::type *p, uint32_t n) {
     RawUnit<DT> r = {};
     if (n == kUnit) {
         if constexpr (DT == PC_F32) {
-            r.w[0] = *reinterpret_cast<const u32x4_any4 *>(p);
-            r.w[1] = *reinterpret_cast<const u32x4_any4 *>(p + 4);
+            r.w[0] = get<u32x4, 4, STREAM>(p);
+            r.w[1] = get<u32x4, 4, STREAM>(p + 4);
         } else {
-            r.w[0] = *reinterpret_cast<const u32x4_any2 *>(p);
+            r.w[0] = get<u32x4, 2, STREAM>(p);
         }
     } else if (n) {
 #pragma unroll
