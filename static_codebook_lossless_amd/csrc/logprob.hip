@@ -17,7 +17,6 @@ constexpr uint32_t kMaxThreads = 1024;
 constexpr uint32_t kMaxWaves = kMaxThreads / kWave;
 constexpr uint32_t kVecs = 4;  // 16-byte loads of a lane on their way together
 constexpr float kLog2E = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-constexpr float kLowest = -3.40282347e38f;
 constexpr float kGone = -1000.0f;  // 2^-1000 is 0 in 32 bits, and 0 times -1000 still 0
 
 template <int DT> constexpr uint32_t kPer = DT == PC_F32 ? 4 : 8;  // elements of 16 bytes
@@ -74,15 +73,20 @@ __device__ __forceinline__ float from_lane(float v, uint32_t lane) { return as_f
 // ---------------------------------------------------------------------------
 
 // Of some elements: the largest one m (-infinity for none), r = m c with
-// c = scale log2(e), rounded and held among the finite numbers, and with
-// u = x c - r the sums of 2^u and of 2^u u.  Everything is relative to the
-// rounded r, so an exponent takes one multiply-add, and what r lost is put
-// right once at the end.  NaN makes s NaN.
+// c = scale log2(e), rounded, and with u = x c - r the sums of 2^u and of
+// 2^u u.  Everything is relative to the rounded r, so an exponent takes one
+// multiply-add, and what r lost (32 at most, below the bound) is put right once
+// at the end.  From the bound on r is held there: neighbouring numbers of 32
+// bits then lie 2^64 apart as probabilities, so only elements equal to m count.
+// NaN makes s NaN.
 struct Soft { float m, r, s, t; };
 
-__device__ __forceinline__ float held(float v) { return fminf(fmaxf(v, kLowest), -kLowest); }
+constexpr float kHeld = 0x1p29f;
 
-__device__ __forceinline__ Soft nothing() { return {-__builtin_inff(), kLowest, 0.0f, 0.0f}; }
+__device__ __forceinline__ float held(float v) { return fminf(fmaxf(v, -kHeld), kHeld); }
+__device__ __forceinline__ bool is_held(float r) { return fabsf(r) == kHeld; }
+
+__device__ __forceinline__ Soft nothing() { return {-__builtin_inff(), -kHeld, 0.0f, 0.0f}; }
 
 // The same sums for another, larger r (fmaxf takes the other operand where one is NaN).
 __device__ __forceinline__ Soft moved(Soft a, float m, float r) {
@@ -92,7 +96,7 @@ __device__ __forceinline__ Soft moved(Soft a, float m, float r) {
 
 // An r that was held stands for any m beyond it: only sums of one m go together.
 __device__ __forceinline__ Soft moved_exactly(Soft a, float m, float r) {
-    if (fabsf(r) == -kLowest && a.m != m) return {m, r, a.s != a.s ? a.s : 0.0f, 0.0f};
+    if (is_held(r) && a.m != m) return {m, r, a.s != a.s ? a.s : 0.0f, 0.0f};
     return moved(a, m, r);
 }
 
@@ -316,7 +320,7 @@ __device__ __forceinline__ void finish(const Args &a, uint64_t row, Soft soft, u
     const float minus = -__builtin_inff();
     const bool empty = soft.m == minus && soft.s == 0.0f;
     // of m: what r lost; 0 where it was held.  +infinity leaves nothing to compare
-    const float lost = fabsf(soft.r) == -kLowest ? 0.0f : __builtin_fmaf(soft.m, a.scale * kLog2E, -soft.r);
+    const float lost = is_held(soft.r) ? 0.0f : __builtin_fmaf(soft.m, a.scale * kLog2E, -soft.r);
     const float bits = soft.m == -minus ? __builtin_nanf("") : log2f(soft.s);
     const float log_sum = kLn2 * (bits - lost);
     auto logp_of = [&](float v) { return empty ? minus : no_more_than_0((v - soft.m) * a.scale - log_sum); };
@@ -480,8 +484,7 @@ __global__ __launch_bounds__(kRowThreads) void rows_kernel(Args a) {
             for (uint32_t j = 0; j < kVecs; ++j) w[j] = next[j];
         }
         const uint32_t key = begin + tid < end ? key_of(soft.m) : 0;
-        if (fabsf(soft.r) == -kLowest && fabsf(soft.m) <= -kLowest) {
-            // so large that neighbouring numbers differ by more than 2^64: those that equal m count
+        if (is_held(soft.r) && fabsf(soft.m) < __builtin_inff()) {  // count those equal to m
             float same = 0.0f;
             for (uint32_t u = begin + tid; u < end; u += threads) {
                 const uint32_t n = count_before(a.vocab, u * N, N);
@@ -595,8 +598,8 @@ __global__ __launch_bounds__(kGradThreads) void grad_kernel(GradArgs a) {
         const uint32_t at = (uint32_t)token;
         // log2 p = x c - r - less:  r is largest c rounded, `less` has what that lost
         const float c = a.scale * kLog2E, r = largest * c;
-        const bool huge = !(fabsf(r) < __builtin_inff());
-        const float less = __builtin_fmaf(log_sum, kLog2E, -__builtin_fmaf(largest, c, -r));
+        const bool huge = !(fabsf(r) < kHeld);
+        const float less = __builtin_fmaf(log_sum, kLog2E, __builtin_fmaf(largest, c, -r));
         const float base = a.scale * (sum + de * entropy), slope = a.scale * de * kLn2;
 #pragma unroll
         for (uint32_t j = 0; j < kGradVecs; ++j) {

@@ -8,13 +8,13 @@ of their last one, and what is returned has their shape.
 """
 from __future__ import annotations
 
+import math
 import operator
 
 import torch
 
 from ._lib import MaskArg, lib
-from .q8 import (Q8, _DTYPES, _FORMATS, PC_BF16, _code, _dtype, _launch, _output, _rows, _same_device, _stored,
-                 _tokens)
+from .q8 import Q8, _DTYPES, _FORMATS, PC_BF16, _code, _dtype, _launch, _rows, _same_device, _tokens
 
 _Y = {None: None, "plain": 0, "stored": 1}
 
@@ -70,23 +70,35 @@ def pc_dropout(x, mask: DropoutMask, out=None) -> torch.Tensor:
     that stays.  The backward pass is the same call on the gradient.  ``out``
     (of x's shape and dtype) receives it and may be ``x``."""
     kind = _dtype(x.dtype, "x")
-    rows, ld = _rows(x, "x")
+    where, n, cols, ld = _flat(x, "x")
     if mask is None:
         raise TypeError("mask must be a DropoutMask")
-    arg = _mask(mask, x.device)
-    out, ld_out = _like(out, x, x.dtype, rows, "out")
-    _launch("pc_dropout", x.device, lib.pc_dropout, rows.data_ptr(), kind, rows.shape[0], rows.shape[1], ld, arg,
-            out.data_ptr(), ld_out)
+    device = x.device
+    arg = _mask(mask, device)
+    out, to, ld_out = _like(out, x, x.dtype, cols, "out")
+    _launch("pc_dropout", device, lib.pc_dropout, where, kind, n, cols, ld, arg, to, ld_out)
     return out
 
 
-def _like(out, x, dtype, rows, what):
-    """(out, its row distance): a tensor of x's shape, ``out`` itself where given."""
+_DENSE = torch.contiguous_format
+
+
+def _flat(t, what):
+    """(address, rows, columns, row distance) of a plain device tensor seen as rows of its last dimension."""
+    if t.is_contiguous() and t.is_cuda and t.dim():
+        cols = t.shape[-1]
+        return t.data_ptr(), t.numel() // cols if cols else math.prod(t.shape[:-1]), cols, cols
+    rows, ld = _rows(t, what)
+    return rows.data_ptr(), rows.shape[0], rows.shape[1], ld
+
+
+def _like(out, x, dtype, cols, what):
+    """(a tensor of x's shape, ``out`` itself where given, its address and row distance)"""
     if out is None:
-        return torch.empty(x.shape, dtype=dtype, device=x.device), rows.shape[1]
-    if out.shape != x.shape:
-        raise ValueError("%s must be %s, not %s" % (what, list(x.shape), list(out.shape)))
-    return out, _output(out, tuple(rows.shape), dtype, x.device, what)[1]
+        out = torch.empty_like(x, dtype=dtype, memory_format=_DENSE)
+        return out, out.data_ptr(), cols
+    where, ld = _same_rows(out, x, dtype, what)
+    return out, where, ld
 
 
 def _same_rows(t, x, dtype, what):
@@ -96,20 +108,27 @@ def _same_rows(t, x, dtype, what):
     if t.shape != x.shape:
         raise ValueError("%s must be %s, not %s" % (what, list(x.shape), list(t.shape)))
     _same_device(x, t, what)
-    rows, ld = _rows(t, what)
-    return rows.data_ptr(), ld
+    where, _, _, ld = _flat(t, what)
+    return where, ld
 
 
-def _weight(weight, cols, device):
+def _weight(weight, cols, device, what="weight"):
     """(address, dtype) of a weight of cols numbers."""
     if weight is None:
         return None, 0
-    kind = _dtype(weight.dtype, "weight")
+    kind = _dtype(weight.dtype, what)
     if weight.shape != (cols,) or not weight.is_contiguous():
-        raise ValueError("weight must be %d contiguous numbers" % cols)
+        raise ValueError("%s must be %d contiguous numbers" % (what, cols))
     if weight.device != device:
-        raise ValueError("weight is on %s, not on %s" % (weight.device, device))
+        raise ValueError("%s is on %s, not on %s" % (what, weight.device, device))
     return weight.data_ptr(), kind
+
+
+def _a_row_each(x, n, device):
+    """One float32 for each row of x."""
+    if x.dim() == 2:
+        return torch.empty(n, dtype=torch.float32, device=device)
+    return torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
 
 
 class RmsNorm:
@@ -135,9 +154,8 @@ def pc_rmsnorm_store(x, weight=None, residual=None, mask=None, eps=1e-6, format=
     what a weight gradient will see.  ``sum_out`` receives the sum and may be
     the residual, or x where their dtypes agree."""
     kind = _dtype(x.dtype, "x")
-    rows, ldx = _rows(x, "x")
+    at, n, cols, ldx = _flat(x, "x")
     device = x.device
-    n, cols = rows.shape
     eps = float(eps)
     arg = _mask(mask, device)
     w, w_kind = _weight(weight, cols, device)
@@ -151,15 +169,14 @@ def pc_rmsnorm_store(x, weight=None, residual=None, mask=None, eps=1e-6, format=
         res, ld_res = _same_rows(residual, x, sum_dtype, "residual")
     total, where, ld_sum = x, None, 0
     if residual is not None or mask is not None:
-        total, ld_sum = _like(sum_out, x, sum_dtype, rows, "sum_out")
-        where = total.data_ptr()
+        total, where, ld_sum = _like(sum_out, x, sum_dtype, cols, "sum_out")
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual or a mask: the sum is x")
     q, sym, scale, code = None, None, None, 0
     if format is not None:
         code = _code(_FORMATS, format, "format")
-        symbols = torch.empty((n, cols), dtype=torch.uint8, device=device)
-        scales = torch.empty((n, -(-cols // 32)), dtype=torch.uint8, device=device)
+        symbols = torch.empty(n, cols, dtype=torch.uint8, device=device)
+        scales = torch.empty(n, -(-cols // 32), dtype=torch.uint8, device=device)
         q = Q8._dense(symbols, scales, format, n, cols, code)
         sym, scale = q.arg.sym, q.arg.scale
     elif y == "stored" or counts is not None:
@@ -172,10 +189,10 @@ def pc_rmsnorm_store(x, weight=None, residual=None, mask=None, eps=1e-6, format=
     if y is not None:
         if dtype is not None:
             to_kind = _dtype(dtype, "dtype")
-        out = torch.empty(x.shape, dtype=dtype or x.dtype, device=device)
+        out = torch.empty_like(x, dtype=dtype, memory_format=_DENSE)
         to = out.data_ptr()
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=device)
-    _launch("pc_rmsnorm_store", device, lib.pc_rmsnorm_store, rows.data_ptr(), kind, n, cols, ldx, res,
+    rstd = _a_row_each(x, n, device)
+    _launch("pc_rmsnorm_store", device, lib.pc_rmsnorm_store, at, kind, n, cols, ldx, res,
             _DTYPES[sum_dtype], ld_res, arg, w, w_kind, eps, where, ld_sum, code, sym, scale,
             None if counts is None else counts.data_ptr(), to, to_kind, cols, int(y == "stored"), rstd.data_ptr())
     return RmsNorm(q, out, total, rstd)
@@ -206,9 +223,8 @@ def pc_rmsnorm_backward(dy, sum, weight, rstd, d_sum=None, mask=None, dtype=None
     or dy's by default).  ``weight_out`` (of weight_dtype) receives the
     weight's gradient; with ``accumulate`` it is added there."""
     kind, out_kind = _dtype(dy.dtype, "dy"), _dtype(weight_dtype, "weight_dtype")
-    rows, ld_dy = _rows(dy, "dy")
+    at, n, cols, ld_dy = _flat(dy, "dy")
     device = dy.device
-    n, cols = rows.shape
     arg = _mask(mask, device)
     w, w_kind = _weight(weight, cols, device)
     kept, kept_ld, stored = None, 0, None
@@ -236,13 +252,11 @@ def pc_rmsnorm_backward(dy, sum, weight, rstd, d_sum=None, mask=None, dtype=None
     if weight_out is not None:
         if weight_out.dtype != weight_dtype:
             raise TypeError("weight_out must be %s, not %s" % (weight_dtype, weight_out.dtype))
-        if weight_out.shape != (cols,) or not weight_out.is_contiguous():
-            raise ValueError("weight_out must be %d contiguous numbers" % cols)
-        _same_device(dy, weight_out, "weight_out")
-    residual = torch.empty(dy.shape, dtype=dtype, device=device)
+        _weight(weight_out, cols, device, "weight_out")
+    residual = torch.empty_like(dy, dtype=dtype, memory_format=_DENSE)
     x, d_x = residual, None
     if mask is not None or dtype != dy.dtype:
-        x = torch.empty(dy.shape, dtype=dy.dtype, device=device)
+        x = torch.empty_like(dy, memory_format=_DENSE)
         d_x = x.data_ptr()
     d_weight, ws, need = weight_out, None, 0
     if weight is not None:
@@ -250,7 +264,7 @@ def pc_rmsnorm_backward(dy, sum, weight, rstd, d_sum=None, mask=None, dtype=None
             d_weight = torch.empty(cols, dtype=weight_dtype, device=device)
         need = lib.pc_rmsnorm_backward_workspace_bytes(n, cols)
         ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    _launch("pc_rmsnorm_backward", device, lib.pc_rmsnorm_backward, rows.data_ptr(), kind, n, cols, ld_dy, kept,
+    _launch("pc_rmsnorm_backward", device, lib.pc_rmsnorm_backward, at, kind, n, cols, ld_dy, kept,
             _DTYPES[dtype], kept_ld, stored, w, w_kind, rstd.data_ptr(), ds, ld_ds, arg, residual.data_ptr(), cols,
             d_x, cols, None if d_weight is None else d_weight.data_ptr(), out_kind, int(accumulate),
             None if ws is None else ws.data_ptr(), need)
@@ -268,13 +282,20 @@ class LogProbs:
     def __init__(self, logp, top_index, top_logp, stats, lead):
         self.logp, self.top_index, self.top_logp, self.stats, self._lead = logp, top_index, top_logp, stats, lead
 
+    def _column(self, k):
+        strides, s = [], 4
+        for size in reversed(self._lead):
+            strides.append(s)
+            s *= size
+        return self.stats.as_strided(self._lead, strides[::-1], self.stats.storage_offset() + k)
+
     @property
     def entropy(self):
-        return self.stats[:, 2].view(self._lead)
+        return self._column(2)
 
     @property
     def lse(self):
-        return self.stats[:, 3].view(self._lead)
+        return self._column(3)
 
 
 def pc_logprobs_workspace_bytes(rows, vocab, top=0, dtype=PC_BF16):
@@ -301,14 +322,13 @@ def pc_logprobs(logits, tokens=None, top=0, scale=1.0, padding=-1, status=None) 
     on the device, zeroed by the caller) to ``PC_ERR_INVALID_ARG``.  Equal
     logits are ordered by their index."""
     kind, scale, padding, top = _dtype(logits.dtype, "logits"), float(scale), operator.index(padding), operator.index(top)
-    rows, ld = _rows(logits, "logits")
+    at, n, vocab, ld = _flat(logits, "logits")
     device, lead = logits.device, logits.shape[:-1]
-    n, vocab = rows.shape
     logp, where, m, width = None, None, 0, 8
     if tokens is not None:
         tokens, m = _picked(tokens, lead, device)
         width = tokens.element_size()
-        logp = torch.empty(tokens.shape, dtype=torch.float32, device=device)
+        logp = torch.empty_like(tokens, dtype=torch.float32)
         where = tokens.data_ptr()
     if top < 0:
         raise ValueError("top is negative")
@@ -316,12 +336,12 @@ def pc_logprobs(logits, tokens=None, top=0, scale=1.0, padding=-1, status=None) 
         raise TypeError("status must be one int32 on the logits' device")
     index = value = None
     if top:
-        index = torch.empty((*lead, top), dtype=torch.int64, device=device)
-        value = torch.empty((*lead, top), dtype=torch.float32, device=device)
-    stats = torch.empty((n, 4), dtype=torch.float32, device=device)
+        index = torch.empty(*lead, top, dtype=torch.int64, device=device)
+        value = torch.empty_like(index, dtype=torch.float32)
+    stats = torch.empty(n, 4, dtype=torch.float32, device=device)
     need = lib.pc_logprobs_workspace_bytes(n, vocab, top, kind)
     ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    _launch("pc_logprobs", device, lib.pc_logprobs, rows.data_ptr(), kind, n, vocab, ld, scale, where, width, m, padding,
+    _launch("pc_logprobs", device, lib.pc_logprobs, at, kind, n, vocab, ld, scale, where, width, m, padding,
             None if logp is None else logp.data_ptr(), top, None if index is None else index.data_ptr(),
             None if value is None else value.data_ptr(), stats.data_ptr(), None if status is None else status.data_ptr(),
             None if ws is None else ws.data_ptr(), need)
@@ -336,9 +356,8 @@ def pc_logprobs_backward(logits, stats, tokens=None, d_logp=None, d_entropy=None
     pass's.  ``out`` (of the logits' shape and dtype) receives it and may be
     ``logits``."""
     kind, scale, padding = _dtype(logits.dtype, "logits"), float(scale), operator.index(padding)
-    rows, ld = _rows(logits, "logits")
+    at, n, vocab, ld = _flat(logits, "logits")
     device, lead = logits.device, logits.shape[:-1]
-    n, vocab = rows.shape
     if stats.dtype != torch.float32 or stats.shape != (n, 4) or not stats.is_contiguous():
         raise TypeError("stats must be [%d, 4] contiguous float32" % n)
     _same_device(logits, stats, "stats")
@@ -352,10 +371,10 @@ def pc_logprobs_backward(logits, stats, tokens=None, d_logp=None, d_entropy=None
         d_logp = _gradient(d_logp, tokens.shape, logits, "d_logp")
     if d_entropy is not None:
         d_entropy = _gradient(d_entropy, lead, logits, "d_entropy")
-    out, ld_out = _like(out, logits, logits.dtype, rows, "out")
-    _launch("pc_logprobs_backward", device, lib.pc_logprobs_backward, rows.data_ptr(), kind, n, vocab, ld, scale,
+    out, to, ld_out = _like(out, logits, logits.dtype, vocab, "out")
+    _launch("pc_logprobs_backward", device, lib.pc_logprobs_backward, at, kind, n, vocab, ld, scale,
             stats.data_ptr(), where, width, m, padding, None if d_logp is None else d_logp.data_ptr(),
-            None if d_entropy is None else d_entropy.data_ptr(), out.data_ptr(), ld_out)
+            None if d_entropy is None else d_entropy.data_ptr(), to, ld_out)
     return out
 
 
