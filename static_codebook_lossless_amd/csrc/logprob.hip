@@ -15,7 +15,7 @@ namespace {
 
 constexpr uint32_t kMaxThreads = 1024;
 constexpr uint32_t kMaxWaves = kMaxThreads / kWave;
-constexpr uint32_t kVecs = 4;  // 16-byte loads of a lane on their way together
+constexpr uint32_t kVecs = 2;  // 16-byte loads of a lane on their way together
 constexpr float kLog2E = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr float kGone = -1000.0f;  // 2^-1000 is 0 in 32 bits, and 0 times -1000 still 0
 
@@ -45,6 +45,19 @@ __device__ __forceinline__ void widen_vec(u32x4 w, float v[kPer<DT>]) {
         r.w[0] = w;
         widen_unit<DT>(r, v);
     }
+}
+
+// The elements from the nth on as -infinity.
+template <int DT>
+__device__ __forceinline__ u32x4 with_end(u32x4 w, uint32_t n) {
+    constexpr uint32_t minus = DT == PC_F32 ? 0xFF800000u : DT == PC_F16 ? 0xFC00u : 0xFF80u;
+#pragma unroll
+    for (uint32_t i = 0; i < kPer<DT>; ++i) {
+        if (i < n) continue;
+        if constexpr (DT == PC_F32) w[i] = minus;
+        else w[i / 2] = i % 2 ? (w[i / 2] & 0xFFFFu) | minus << 16 : (w[i / 2] & 0xFFFF0000u) | minus;
+    }
+    return w;
 }
 
 template <int DT>
@@ -198,16 +211,20 @@ __device__ __forceinline__ void descend(T &v) {
         exchange<1>(v, true);
 }
 
-// A lane's value each, in descending order.
+// A lane's value each, in descending order.  Only the first `n` are not 0: the
+// steps for 16 and 32 lanes leave the first half-rows and rows in order, and
+// are enough for as many.
 template <class T>
-__device__ __forceinline__ T sorted(T v) {
+__device__ __forceinline__ T sorted(T v, uint32_t n = kWave) {
     const uint32_t l = threadIdx.x;
     exchange<1>(v, !(l & 2));
     exchange<2>(v, !(l & 4)), exchange<1>(v, !(l & 4));
     exchange<4>(v, !(l & 8)), exchange<2>(v, !(l & 8)), exchange<1>(v, !(l & 8));
     exchange<8>(v, !(l & 16)), exchange<4>(v, !(l & 16)), exchange<2>(v, !(l & 16)), exchange<1>(v, !(l & 16));
+    if (n <= 16) return v;
     exchange<16>(v, !(l & 32)), exchange<8>(v, !(l & 32)), exchange<4>(v, !(l & 32)), exchange<2>(v, !(l & 32)),
         exchange<1>(v, !(l & 32));
+    if (n <= 32) return v;
     descend(v);
     return v;
 }
@@ -243,7 +260,7 @@ __device__ __forceinline__ uint64_t lane_of(uint64_t v, uint32_t lane) {
 __device__ __forceinline__ void settle(Best &b, uint32_t top) {
     const uint32_t lane = threadIdx.x % kWave;
     wave_order();
-    const uint64_t v = sorted(lane < b.count ? b.pool[lane] : 0), rest = b.pool[kWave + lane];
+    const uint64_t v = sorted(lane < b.count ? b.pool[lane] : 0, b.count), rest = b.pool[kWave + lane];
     wave_order();
     b.pool[lane] = rest;
     wave_order();
@@ -270,24 +287,27 @@ __device__ __forceinline__ int64_t token_at(const void *tokens, int token_bytes,
     return token_bytes == 8 ? static_cast<const int64_t *>(tokens)[i] : static_cast<const int32_t *>(tokens)[i];
 }
 
-// Joins the waves' sums and lists in LDS; wave 0 has the result.
-template <bool TOP>
-__device__ __forceinline__ void join_waves(Soft &soft, uint64_t &best, float c, Soft *softs, uint64_t *lists) {
+// Joins the waves' sums; wave 0 has the result.
+__device__ __forceinline__ void join_softs(Soft &soft, float c, Soft *softs) {
     const uint32_t wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave, waves = blockDim.x / kWave;
     if (waves == 1) return;
     if (lane == 0) softs[wave] = soft;
-    if constexpr (TOP) {
-        lists[wave * kWave + lane] = best;
-        for (uint32_t half = waves / 2; half; half /= 2) {
-            __syncthreads();
-            if (wave < half) {
-                best = merged(best, lists[(wave + half) * kWave + lane]);
-                lists[wave * kWave + lane] = best;
-            }
-        }
-    }
     __syncthreads();
     if (wave == 0) soft = wave_soft(lane < waves ? softs[lane] : nothing(), c);
+}
+
+// Joins the waves' lists (a power of two); wave 0 has the result.
+__device__ __forceinline__ uint64_t join_lists(uint64_t best, uint64_t *lists) {
+    const uint32_t wave = uniform(threadIdx.x / kWave), lane = threadIdx.x % kWave, waves = blockDim.x / kWave;
+    lists[wave * kWave + lane] = best;
+    for (uint32_t half = waves / 2; half; half /= 2) {
+        __syncthreads();
+        if (wave < half) {
+            best = merged(best, lists[(wave + half) * kWave + lane]);
+            lists[wave * kWave + lane] = best;
+        }
+    }
+    return best;
 }
 
 // What a lane of the finishing wave needs for its token, loaded early.
@@ -343,81 +363,115 @@ __device__ __forceinline__ void finish(const Args &a, uint64_t row, Soft soft, u
 
 constexpr uint32_t kRowThreads = 256;
 
-// The row's `top` largest elements, once every lane knows the largest of the
-// units it has read (its strip, every `threads`th unit from its own on).
+struct TopArea {
+    uint64_t lists[kRowThreads], pools[kRowThreads / kWave * kPool], first[kWave];
+    uint32_t keys[kRowThreads], found;
+    uint8_t strips[kRowThreads];
+};
+
+__device__ __forceinline__ uint32_t lanes_before(uint64_t mask) {
+    return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
+// The row's `top` largest elements in wave 0, a lane each in descending order,
+// once every lane knows the largest of the units it has read (its strip, every
+// `threads`th unit from its own on).
 //
 // The `top`th largest of these lanes' largest is at most the `top`th of all
 // elements, and hardly less: the largest elements mostly lie in strips of their
 // own.  Strips whose largest is below it hold none of them; of the few others
 // the wave reads all units again, side by side, and takes what is not below the
-// bound.  So the pass over the row does nothing for the alternatives; a wave
-// that compares every element with the least it has kept so far does twice the
-// work (2048 x 32000 bf16, 20 of them: 66 us, without them 31).
+// bound: with 256 strips little more than `top` elements, which one wave sorts.
+// Where ties make that more than 64, each wave keeps a list of its own.  So the
+// pass over the row does nothing for the alternatives; comparing every element
+// with the least one kept so far doubles its work (2048 x 32000 bf16, 20 of
+// them: 66 us, without them 31).
 template <int DT>
 __device__ __forceinline__ uint64_t largest_elements(const Args &a, const typename Plain<DT>::type *x, uint32_t begin,
-                                                     uint32_t end, uint32_t key, uint32_t *keys, uint64_t *pool,
-                                                     uint8_t *strips) {
+                                                     uint32_t end, uint32_t key, TopArea &area) {
     constexpr uint32_t N = kPer<DT>;
     const uint32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave), threads = blockDim.x;
     uint32_t best_keys = sorted(key);
     if (threads > kWave) {
-        keys[threadIdx.x] = best_keys;
+        area.keys[threadIdx.x] = best_keys;
+        if (threadIdx.x == 0) area.found = 0;
         __syncthreads();
         for (uint32_t w = 0; w < threads / kWave; ++w)
-            if (w != wave) best_keys = merged(best_keys, keys[w * kWave + lane]);
+            if (w != wave) best_keys = merged(best_keys, area.keys[w * kWave + lane]);
     }
     const uint32_t bound = max(1u, from_lane(best_keys, a.top - 1));  // 0: fewer lanes than that have read any
+    const float low = bound > key_of(-__builtin_inff()) ? of_key(bound) : __builtin_nanf("");  // NaN: all may count
     const uint64_t likely = __ballot(key >= bound);
     const uint32_t count = (uint32_t)__builtin_popcountll(likely);
-    strips += wave * kWave;
-    if (key >= bound)
-        strips[__builtin_amdgcn_mbcnt_hi((uint32_t)(likely >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)likely, 0))] =
-            (uint8_t)lane;
+    uint8_t *strips = area.strips + wave * kWave;
+    if (key >= bound) strips[lanes_before(likely)] = (uint8_t)lane;
     wave_order();
-    Best b = {0, 0, pool + wave * kPool, 0};
     // `wide` lanes to a strip (a power of two), 64 / wide strips at a time
     const uint32_t length = (end - begin + threads - 1) / threads;
     uint32_t log_wide = 0;
     while (log_wide < 6 && (1u << log_wide) < length) ++log_wide;
     const uint32_t wide = 1u << log_wide, together = kWave >> log_wide;
-    for (uint32_t s = 0; s < count; s += together) {
-        const uint32_t strip = s + (lane >> log_wide);
-        const uint32_t first = begin + wave * kWave + strips[min(strip, kWave - 1)];
-        for (uint32_t k0 = 0; k0 < length; k0 += wide) {
-            const uint32_t k = k0 + (lane & (wide - 1));
-            const uint32_t u = first + k * threads;
-            const uint32_t n = strip < count && k < length && u < end ? count_before(a.vocab, u * N, N) : 0;
+    const uint32_t turns = (length + wide - 1) / wide, parts = (count + together - 1) / together * turns;
+    auto load = [&](uint32_t q, uint32_t &u, uint32_t &n) {
+        const uint32_t s = q / turns;
+        const uint32_t strip = s * together + (lane >> log_wide), k = (q - s * turns) * wide + (lane & (wide - 1));
+        u = begin + wave * kWave + strips[min(strip, kWave - 1)] + k * threads;
+        n = q < parts && strip < count && k < length && u < end ? count_before(a.vocab, u * N, N) : 0;
+        return load_vec<DT, false>(x + (uint64_t)u * N, n);
+    };
+    Best b = {0, 0, area.pools + wave * kPool, 0};
+    // first into one area for all waves; where that is too small, again into each wave's own list
+    for (bool shared = threads > kWave;; shared = false) {
+        uint32_t u, n;
+        u32x4 w = load(0, u, n);
+        for (uint32_t q = 0; q < parts; ++q) {
+            uint32_t next_u, next_n;
+            const u32x4 next = load(q + 1, next_u, next_n);
             float v[N];
-            widen_vec<DT>(load_vec<DT, false>(x + (uint64_t)u * N, n), v);
+            widen_vec<DT>(w, v);
 #pragma unroll
             for (uint32_t i = 0; i < N; ++i) {
+                if (__ballot(!(v[i] < low)) == 0) continue;
                 const uint32_t vk = key_of(v[i]);
                 const uint64_t p = packed(vk, u * N + i);
                 const bool in = i < n && vk >= bound && p > b.least;
                 const uint64_t all = __ballot(in);
-                if (all) {
-                    if (in)
-                        b.pool[b.count + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32),
-                                                                   __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0))] = p;
+                if (!all) continue;
+                uint64_t *to = b.pool;
+                uint32_t at = b.count, most = kPool;
+                if (shared) {
+                    if (lane == 0) at = atomicAdd(&area.found, (uint32_t)__builtin_popcountll(all));
+                    at = uniform(at);
+                    to = area.first;
+                    most = kWave;
+                }
+                at += lanes_before(all);
+                if (in && at < most) to[at] = p;
+                if (!shared) {
                     b.count += (uint32_t)__builtin_popcountll(all);
                     if (b.count >= kWave) settle(b, a.top);
                 }
             }
+            w = next;
+            u = next_u;
+            n = next_n;
         }
+        if (!shared) break;
+        __syncthreads();
+        const uint32_t found = uniform(area.found);
+        if (found <= kWave) return wave == 0 ? sorted(lane < found ? area.first[lane] : 0, found) : 0;
     }
     if (b.count) settle(b, a.top);
-    return b.list;
+    return threads > kWave ? join_lists(b.list, area.lists) : b.list;
 }
 
 // A workgroup takes a row, or one of `splits` stretches of it.
 template <int DT, bool TOP, bool STREAM>
-__global__ __launch_bounds__(kRowThreads) void rows_kernel(Args a) {
+__global__ __launch_bounds__(kRowThreads, TOP ? 6 : 8) void rows_kernel(Args a) {
     typedef typename Plain<DT>::type T;
     constexpr uint32_t N = kPer<DT>;
     __shared__ Soft softs[kMaxWaves];
-    __shared__ uint64_t lists[TOP ? kRowThreads : 1], pools[TOP ? kRowThreads / kWave * kPool : 1];
-    __shared__ uint32_t keys[TOP ? kRowThreads : 1];
-    __shared__ uint8_t strips[TOP ? kRowThreads : 1];
+    __shared__ std::conditional_t<TOP, TopArea, char> area;
     const uint32_t tid = threadIdx.x, threads = blockDim.x, step = threads * kVecs;
     const float c = a.scale * kLog2E;
     const uint64_t total = a.rows * a.splits;
@@ -443,19 +497,18 @@ __global__ __launch_bounds__(kRowThreads) void rows_kernel(Args a) {
         for (uint32_t base = begin; base < end; base += step) {
             u32x4 next[kVecs];
             load(base + step, next);
-            float v[kVecs][N], m = soft.m;
+            // the maximum first, then the sums, each from the elements as loaded: wide ones
+            // of both loads would take the registers of two of the eight waves
+            float m = soft.m;
 #pragma unroll
             for (uint32_t j = 0; j < kVecs; ++j) {
                 const uint32_t u = base + j * threads + tid;
                 const uint32_t n = u < end ? count_before(a.vocab, u * N, N) : 0;
-                widen_vec<DT>(w[j], v[j]);
-                if (n != N) {
+                if (n != N) w[j] = with_end<DT>(w[j], n);
+                float v[N];
+                widen_vec<DT>(w[j], v);
 #pragma unroll
-                    for (uint32_t i = 0; i < N; ++i)
-                        if (i >= n) v[j][i] = -__builtin_inff();
-                }
-#pragma unroll
-                for (uint32_t i = 0; i < N; ++i) m = fmaxf(m, v[j][i]);
+                for (uint32_t i = 0; i < N; ++i) m = fmaxf(m, v[i]);
             }
             const float r = held(m * c);
             soft = moved(soft, m, r);
@@ -463,9 +516,12 @@ __global__ __launch_bounds__(kRowThreads) void rows_kernel(Args a) {
                 s = t = 0.0f;
 #pragma unroll
                 for (uint32_t j = 0; j < kVecs; ++j) {
+                    asm volatile("" : "+v"(w[j]));
+                    float v[N];
+                    widen_vec<DT>(w[j], v);
 #pragma unroll
                     for (uint32_t i = 0; i < N; ++i) {
-                        const float y = __builtin_fmaf(v[j][i], c, -r), e = __builtin_amdgcn_exp2f(y);
+                        const float y = __builtin_fmaf(v[i], c, -r), e = __builtin_amdgcn_exp2f(y);
                         s += e;
                         t += e * (decltype(mind)::value ? fmaxf(y, kGone) : y);
                     }
@@ -498,8 +554,8 @@ __global__ __launch_bounds__(kRowThreads) void rows_kernel(Args a) {
         }
         soft = wave_soft(soft, c);
         uint64_t list = 0;
-        if constexpr (TOP) list = largest_elements<DT>(a, x, begin, end, key, keys, pools, strips);
-        join_waves<TOP>(soft, list, c, softs, lists);
+        if constexpr (TOP) list = largest_elements<DT>(a, x, begin, end, key, area);
+        join_softs(soft, c, softs);
         if (tid < kWave) {
             if (a.splits == 1) {
                 finish<TOP>(a, row, soft, list, p);
@@ -531,7 +587,8 @@ __global__ __launch_bounds__(kMaxThreads) void join_kernel(Args a) {
         for (uint32_t s = wave; s < a.splits; s += waves)
             best = merged(best, lane < a.top ? a.best[(row * a.splits + s) * a.top + lane] : 0);
     }
-    join_waves<TOP>(soft, best, c, softs, lists);
+    if constexpr (TOP) best = join_lists(best, lists);
+    join_softs(soft, c, softs);
     if (wave == 0) finish<TOP>(a, row, soft, best, p);
 }
 
@@ -651,7 +708,7 @@ struct Plan { uint32_t threads, splits, per_split; };
 Plan plan_rows(uint64_t rows, uint64_t vocab, int dtype) {
     Plan p;
     const uint32_t units = units_of(vocab, dtype);
-    p.threads = units <= kRowThreads || (rows >= 4096 && units <= 4096) ? kWave : kRowThreads;
+    p.threads = units <= kRowThreads || (rows >= 4096 && units <= 1024) ? kWave : kRowThreads;
     p.splits = 1;
     p.per_split = units;
     const uint32_t least = kRowThreads * kVecs;
