@@ -160,6 +160,14 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 
 __device__ __forceinline__ float of_key(uint32_t k) { return as_f32(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    v = max(v, dpp_u32<0xB1>(v));
+    v = max(v, dpp_u32<0x4E>(v));
+    v = max(v, dpp_u32<0x141>(v));
+    v = max(v, dpp_u32<0x140>(v));
+    return max(max(from_lane(v, 0), from_lane(v, 16)), max(from_lane(v, 32), from_lane(v, 48)));
+}
+
 // An element as one number: larger ones first, of equal ones that of the lower
 // index.  0 stands for no element.
 __device__ __forceinline__ uint64_t packed(uint32_t key, uint32_t index) {
@@ -363,14 +371,49 @@ __device__ __forceinline__ void finish(const Args &a, uint64_t row, Soft soft, u
 
 constexpr uint32_t kRowThreads = 256;
 
+constexpr uint32_t kFirst = 2 * kWave;
+
 struct TopArea {
-    uint64_t lists[kRowThreads], pools[kRowThreads / kWave * kPool], first[kWave];
+    uint64_t lists[kRowThreads], pools[kRowThreads / kWave * kPool], first[kFirst];
     uint32_t keys[kRowThreads], found;
     uint8_t strips[kRowThreads];
 };
 
 __device__ __forceinline__ uint32_t lanes_before(uint64_t mask) {
     return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+}
+
+// The wave's largest elements of those not below the bound, from the lanes'
+// own strips, whose indices grow from step to step: an element equal to the
+// `top`th one so far has no place any more.
+template <int DT>
+__device__ __forceinline__ uint64_t largest_in_order(const Args &a, const typename Plain<DT>::type *x, uint32_t begin,
+                                                     uint32_t end, uint32_t bound, uint64_t *pool) {
+    constexpr uint32_t N = kPer<DT>;
+    Best b = {0, 0, pool, 0};
+    for (uint32_t u0 = begin; u0 < end; u0 += blockDim.x) {
+        const uint32_t u = u0 + threadIdx.x, n = u < end ? count_before(a.vocab, u * N, N) : 0;
+        float v[N];
+        widen_vec<DT>(load_vec<DT, false>(x + (uint64_t)u * N, n), v);
+        const uint32_t least = max(bound, (uint32_t)(b.least >> 32) + 1);
+        uint32_t most = 0;
+#pragma unroll
+        for (uint32_t i = 0; i < N; ++i) most = max(most, i < n ? key_of(v[i]) : 0);
+        if (__ballot(most >= least) == 0) continue;
+#pragma unroll
+        for (uint32_t i = 0; i < N; ++i) {
+            const uint32_t key = key_of(v[i]);
+            const uint64_t p = packed(key, u * N + i);
+            const bool in = i < n && key >= bound && p > b.least;
+            const uint64_t all = __ballot(in);
+            if (!all) continue;
+            if (in) b.pool[b.count + lanes_before(all)] = p;
+            b.count += (uint32_t)__builtin_popcountll(all);
+            if (b.count >= kWave) settle(b, a.top);
+        }
+    }
+    if (b.count) settle(b, a.top);
+    return b.list;
 }
 
 // The row's `top` largest elements in wave 0, a lane each in descending order,
@@ -382,25 +425,32 @@ __device__ __forceinline__ uint32_t lanes_before(uint64_t mask) {
 // own.  Strips whose largest is below it hold none of them; of the few others
 // the wave reads all units again, side by side, and takes what is not below the
 // bound: with 256 strips little more than `top` elements, which one wave sorts.
-// Where ties make that more than 64, each wave keeps a list of its own.  So the
-// pass over the row does nothing for the alternatives; comparing every element
-// with the least one kept so far doubles its work (2048 x 32000 bf16, 20 of
-// them: 66 us, without them 31).
+// Where ties make them more than 128 (a masked stretch is equal throughout),
+// the waves go over their strips in order.  So the pass over the row does
+// nothing for the alternatives; comparing every element with the least one kept
+// so far doubles its work (2048 x 32000 bf16, 20 of them: 66 us, without them 31).
 template <int DT>
 __device__ __forceinline__ uint64_t largest_elements(const Args &a, const typename Plain<DT>::type *x, uint32_t begin,
                                                      uint32_t end, uint32_t key, TopArea &area) {
     constexpr uint32_t N = kPer<DT>;
     const uint32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave), threads = blockDim.x;
-    uint32_t best_keys = sorted(key);
+    const uint32_t nothing = key_of(-__builtin_inff());
+    uint32_t best_keys = a.top == 1 ? wave_max(key) : sorted(key);
     if (threads > kWave) {
         area.keys[threadIdx.x] = best_keys;
         if (threadIdx.x == 0) area.found = 0;
         __syncthreads();
-        for (uint32_t w = 0; w < threads / kWave; ++w)
-            if (w != wave) best_keys = merged(best_keys, area.keys[w * kWave + lane]);
+        for (uint32_t w = 0; w < threads / kWave; ++w) {
+            const uint32_t other = area.keys[w * kWave + lane];
+            if (w != wave) best_keys = a.top == 1 ? max(best_keys, other) : merged(best_keys, other);
+        }
     }
     const uint32_t bound = max(1u, from_lane(best_keys, a.top - 1));  // 0: fewer lanes than that have read any
-    const float low = bound > key_of(-__builtin_inff()) ? of_key(bound) : __builtin_nanf("");  // NaN: all may count
+    if (from_lane(best_keys, 0) == nothing) {  // masked throughout: the first elements
+        const uint64_t index = (uint64_t)begin * N + lane;
+        return wave == 0 && index < min((uint64_t)end * N, (uint64_t)a.vocab) ? packed(nothing, (uint32_t)index) : 0;
+    }
+    const float low = bound > nothing ? of_key(bound) : __builtin_nanf("");  // NaN: all may count
     const uint64_t likely = __ballot(key >= bound);
     const uint32_t count = (uint32_t)__builtin_popcountll(likely);
     uint8_t *strips = area.strips + wave * kWave;
@@ -419,50 +469,49 @@ __device__ __forceinline__ uint64_t largest_elements(const Args &a, const typena
         n = q < parts && strip < count && k < length && u < end ? count_before(a.vocab, u * N, N) : 0;
         return load_vec<DT, false>(x + (uint64_t)u * N, n);
     };
-    Best b = {0, 0, area.pools + wave * kPool, 0};
-    // first into one area for all waves; where that is too small, again into each wave's own list
-    for (bool shared = threads > kWave;; shared = false) {
-        uint32_t u, n;
-        u32x4 w = load(0, u, n);
-        for (uint32_t q = 0; q < parts; ++q) {
-            uint32_t next_u, next_n;
-            const u32x4 next = load(q + 1, next_u, next_n);
-            float v[N];
-            widen_vec<DT>(w, v);
+    uint32_t found = 0, u, n;
+    u32x4 w = load(0, u, n);
+    for (uint32_t q = 0; q < parts && found <= kFirst; ++q) {
+        uint32_t next_u, next_n;
+        const u32x4 next = load(q + 1, next_u, next_n);
+        float v[N];
+        widen_vec<DT>(w, v);
 #pragma unroll
-            for (uint32_t i = 0; i < N; ++i) {
-                if (__ballot(!(v[i] < low)) == 0) continue;
-                const uint32_t vk = key_of(v[i]);
-                const uint64_t p = packed(vk, u * N + i);
-                const bool in = i < n && vk >= bound && p > b.least;
-                const uint64_t all = __ballot(in);
-                if (!all) continue;
-                uint64_t *to = b.pool;
-                uint32_t at = b.count, most = kPool;
-                if (shared) {
-                    if (lane == 0) at = atomicAdd(&area.found, (uint32_t)__builtin_popcountll(all));
-                    at = uniform(at);
-                    to = area.first;
-                    most = kWave;
-                }
-                at += lanes_before(all);
-                if (in && at < most) to[at] = p;
-                if (!shared) {
-                    b.count += (uint32_t)__builtin_popcountll(all);
-                    if (b.count >= kWave) settle(b, a.top);
-                }
+        for (uint32_t i = 0; i < N; ++i) {
+            if (__ballot(!(v[i] < low)) == 0) continue;
+            const uint32_t vk = key_of(v[i]);
+            const bool in = i < n && vk >= bound;
+            const uint64_t all = __ballot(in);
+            if (!all) continue;
+            uint32_t at = found;
+            if (threads > kWave) {
+                if (lane == 0) at = atomicAdd(&area.found, (uint32_t)__builtin_popcountll(all));
+                at = uniform(at);
             }
-            w = next;
-            u = next_u;
-            n = next_n;
+            found = at + (uint32_t)__builtin_popcountll(all);
+            at += lanes_before(all);
+            if (in && at < kFirst) area.first[at] = packed(vk, u * N + i);
         }
-        if (!shared) break;
-        __syncthreads();
-        const uint32_t found = uniform(area.found);
-        if (found <= kWave) return wave == 0 ? sorted(lane < found ? area.first[lane] : 0, found) : 0;
+        w = next;
+        u = next_u;
+        n = next_n;
     }
-    if (b.count) settle(b, a.top);
-    return threads > kWave ? join_lists(b.list, area.lists) : b.list;
+    if (threads > kWave) {
+        __syncthreads();
+        found = uniform(area.found);
+    } else {
+        wave_order();
+    }
+    if (found > kFirst) {
+        const uint64_t list = largest_in_order<DT>(a, x, begin, end, bound, area.pools + wave * kPool);
+        return threads > kWave ? join_lists(list, area.lists) : list;
+    }
+    if (wave) return 0;
+    uint64_t list = lane < found ? area.first[lane] : 0;
+    if (found == 1) return list;
+    list = sorted(list, found);
+    if (found <= kWave) return list;
+    return merged(list, sorted(kWave + lane < found ? area.first[kWave + lane] : 0, found - kWave));
 }
 
 // A workgroup takes a row, or one of `splits` stretches of it.

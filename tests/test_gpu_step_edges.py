@@ -566,3 +566,56 @@ def test_binding_refuses():
         with pytest.raises(error):
             call()
             raise AssertionError("call %d passed" % k)
+
+
+# -- forms that only the C entries have ------------------------------------------------
+
+@pytest.mark.parametrize("rows,cols", [(70, 264), (9, 8200), (5, 8191), (4, 33000), (3, 40001)])
+def test_norm_backward_in_place(rows, cols):
+    """The residual's gradient over the one that comes in, x's over y's."""
+    lib = pc._lib.lib
+    rng = np.random.default_rng(51)
+    dy, h, ds = (activation(rng, rows, cols, "bf16") for _ in range(3))
+    w, rstd = torch.rand(cols, device=DEV), torch.rand(rows, device=DEV)
+    mask = pc.DropoutMask(0.3, 4)
+    want = pc.pc_rmsnorm_backward(dy, h, w, rstd, d_sum=ds, mask=mask)
+    need = pc.pc_rmsnorm_backward_workspace_bytes(rows, cols)
+    ws, dw = torch.empty(need, dtype=torch.uint8, device=DEV), torch.empty(cols, device=DEV)
+    st = lib.pc_rmsnorm_backward(dy.data_ptr(), pc.PC_BF16, rows, cols, cols, h.data_ptr(), pc.PC_BF16, cols, None,
+                                 w.data_ptr(), pc.PC_F32, rstd.data_ptr(), ds.data_ptr(), cols, mask.arg, ds.data_ptr(), cols,
+                                 dy.data_ptr(), cols, dw.data_ptr(), pc.PC_F32, 0, ws.data_ptr(), need,
+                                 torch.cuda.current_stream().cuda_stream)
+    assert st == pc.PC_OK
+    assert torch.equal(ds, want.residual) and torch.equal(dy, want.x) and torch.equal(dw, want.weight)
+
+
+@pytest.mark.parametrize("rows,cols", [(70, 264), (5, 8191), (3, 40001), (300, 96)])
+def test_norm_without_its_sum(rows, cols):
+    """A last norm, whose sum nothing reads: the same y; and a call that wants nothing but rstd."""
+    lib = pc._lib.lib
+    rng = np.random.default_rng(52)
+    x, res = activation(rng, rows, cols, "f16"), activation(rng, rows, cols, "f32")
+    mask = pc.DropoutMask(0.3, 4)
+    want = pc.pc_rmsnorm_store(x, None, res, mask, y="plain")
+    y, rstd = torch.empty_like(x), torch.empty(rows, device=DEV)
+    stream = torch.cuda.current_stream().cuda_stream
+    st = lib.pc_rmsnorm_store(x.data_ptr(), pc.PC_F16, rows, cols, cols, res.data_ptr(), pc.PC_F32, cols, mask.arg, None, 0,
+                              1e-6, None, 0, 0, None, None, None, y.data_ptr(), pc.PC_F16, cols, 0, None, stream)
+    assert st == pc.PC_OK and torch.equal(y, want.y)
+    st = lib.pc_rmsnorm_store(x.data_ptr(), pc.PC_F16, rows, cols, cols, res.data_ptr(), pc.PC_F32, cols, mask.arg, None, 0,
+                              1e-6, None, 0, 0, None, None, None, None, 0, 0, 0, rstd.data_ptr(), stream)
+    assert st == pc.PC_OK and torch.equal(rstd, want.rstd)
+    bare = pc.pc_rmsnorm_store(x, residual=res, mask=mask, format=None)
+    assert bare.q is None and bare.y is None and torch.equal(bare.sum, want.sum)
+
+
+def test_masked_stretches_and_alternatives():
+    """Splits that are masked throughout, with more alternatives than the rest of the row has tokens."""
+    for vocab, left in ((40000, 3), (40000, 30), (150001, 10), (9000, 64)):
+        x = torch.full((3, vocab), -INF, device=DEV)
+        at = torch.linspace(0, vocab - 1, left, device=DEV).long()
+        x[0, at] = torch.arange(left, device=DEV, dtype=torch.float32)
+        x[1, vocab // 2:vocab // 2 + left] = 1.0
+        x[2, -left:] = torch.randn(left, device=DEV)
+        r = pc.pc_logprobs(x, top=64)
+        assert np.array_equal(r.top_index.cpu().numpy(), np.argsort(-np64(x), axis=1, kind="stable")[:, :64]), (vocab, left)
