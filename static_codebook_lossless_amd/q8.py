@@ -72,10 +72,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+# the same without torch.cuda.current_device's check for a device, as every caller has a tensor there
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _launch(what, device, fn, *args):
     """Call ``fn`` on the device's current stream."""
     index = device.index
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
