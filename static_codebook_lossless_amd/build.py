@@ -38,9 +38,9 @@ def build(verbose: bool = False) -> str:
     tmp = LIB + ".tmp%d" % os.getpid()
     with tempfile.TemporaryDirectory() as d, concurrent.futures.ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
         objects = [(src, os.path.join(d, os.path.basename(src) + ".o")) for src in sources()]
-        # the sources share nothing on the device, so each is compiled by itself
+        # the sources share nothing on the device, so each is compiled by itself, large ones first
         list(pool.map(lambda so: run([hipcc] + HIPCC_FLAGS + ["-I", INCLUDE, "-I", CSRC, "-c", "-o", so[1], so[0]]),
-                      objects))
+                      sorted(objects, key=lambda so: -os.path.getsize(so[0]))))
         run([hipcc, "-shared", "-fPIC", "--offload-arch=" + ARCH, "-o", tmp] + [o for _, o in objects])
     os.replace(tmp, LIB)
     return LIB

@@ -10,6 +10,7 @@ namespace pc {
 constexpr uint32_t kMaxThreads = 1024;
 constexpr uint32_t kCountBlocks = 256;  // workgroups of the counting form
 constexpr uint32_t kGradThreads = 256;
+constexpr uint32_t kOnceColumns = 64;  // of a workgroup, where rows and columns share a launch
 constexpr uint32_t kColumnThreads = 256;  // weight gradient of long rows
 constexpr uint32_t kColumnWaves = kColumnThreads / kWave;
 
@@ -38,6 +39,10 @@ struct GradArgs {
     int weight_kind, format;
     float per_col;  // 1 / cols
     MaskArg mask;
+    // rows and columns in one launch
+    void *d_weight;
+    int d_weight_kind, accumulate;
+    uint32_t row_blocks;
 };
 
 // How a call is split, by rules on sizes alone (norm.hip).
@@ -50,7 +55,7 @@ struct GradPlan {
     uint32_t per, team, threads, blocks;  // per == 0: long rows
     uint32_t parts;                       // rows of partial sums
     uint32_t column_blocks, slices;       // of the long rows' weight gradient
-    bool whole, streams;
+    bool whole, streams, once;            // once: blocks for rows and for columns in one launch
 };
 
 

@@ -121,6 +121,26 @@ GradPlan plan_grad(uint64_t rows, uint64_t cols, bool f32, uint64_t bytes) {
     return p;
 }
 
+// Rows and columns in one launch, by sizes alone.
+constexpr uint64_t kOnceRows = 512, kOnceElements = 1ull << 21;
+
+bool once_fits(uint64_t rows, uint64_t cols) {
+    return rows <= kOnceRows && rows * cols <= kOnceElements && units_of(cols) <= kMaxThreads;
+}
+
+// The same plan for one launch; the columns' workgroups come after the rows'.
+GradPlan plan_once(uint64_t rows, uint64_t cols, uint32_t &row_blocks) {
+    GradPlan p = {};
+    p.once = true;
+    p.per = 1;
+    p.team = team_for(units_of(cols), 1, false);
+    p.threads = lanes_for(p.team, kGradThreads);
+    const uint64_t teams = p.threads / p.team;
+    row_blocks = (uint32_t)((rows + teams - 1) / teams);
+    p.blocks = row_blocks + (uint32_t)((cols + kOnceColumns - 1) / kOnceColumns);
+    return p;
+}
+
 uint64_t partial_width(uint64_t cols) { return (cols + 3) / 4 * 4; }
 
 }  // namespace
@@ -159,6 +179,7 @@ hipError_t launch_rmsnorm_store(const RmsNorm &c, hipStream_t stream) {
 }
 
 uint64_t rmsnorm_backward_workspace(uint64_t rows, uint64_t cols) {
+    if (once_fits(rows, cols)) return 0;
     // the largest of any types'
     uint32_t parts = 0;
     for (int f32 = 0; f32 < 2; ++f32)
@@ -169,9 +190,11 @@ uint64_t rmsnorm_backward_workspace(uint64_t rows, uint64_t cols) {
 
 hipError_t launch_rmsnorm_backward(const RmsNormGrad &c, hipStream_t stream) {
     const uint64_t kept = c.stored ? 1 : size_of(c.sum_dtype), d_sum = c.d_sum ? size_of(c.sum_dtype) : 0;
-    const GradPlan p = plan_grad(c.rows, c.cols, c.sum_dtype == PC_F32,
-                                 c.rows * c.cols * (size_of(c.dtype) + kept + d_sum));
     GradArgs a = {};
+    const bool once = c.d_weight && c.rows && once_fits(c.rows, c.cols);
+    const GradPlan p = once ? plan_once(c.rows, c.cols, a.row_blocks)
+                            : plan_grad(c.rows, c.cols, c.sum_dtype == PC_F32,
+                                        c.rows * c.cols * (size_of(c.dtype) + kept + d_sum));
     a.dy = c.dy;
     a.sum = c.sum;
     a.ld_sum = c.ld_sum;
@@ -188,7 +211,10 @@ hipError_t launch_rmsnorm_backward(const RmsNormGrad &c, hipStream_t stream) {
     a.rstd = c.rstd;
     a.d_res = c.d_res;
     a.d_x = c.d_x;
-    a.partial = c.d_weight ? static_cast<float *>(c.ws) : nullptr;
+    a.partial = c.d_weight && !once ? static_cast<float *>(c.ws) : nullptr;
+    a.d_weight = c.d_weight;
+    a.d_weight_kind = c.d_weight_dtype;
+    a.accumulate = c.accumulate;
     a.rows = c.rows;
     a.ld_dy = c.ld_dy;
     a.ld_d_sum = c.ld_d_sum;
@@ -210,7 +236,7 @@ hipError_t launch_rmsnorm_backward(const RmsNormGrad &c, hipStream_t stream) {
             e = wide ? norm_backward<PC_BF16, PC_F32>(a, p, stream) : norm_backward<PC_BF16, PC_BF16>(a, p, stream);
         if (e != hipSuccess) return e;
     }
-    if (c.d_weight) {
+    if (c.d_weight && !once) {
         const dim3 grid((uint32_t)std::min<uint64_t>((c.cols + kJoinColumns - 1) / kJoinColumns, 1u << 16));
         with_dtype(c.d_weight_dtype, [&](auto d) {
             constexpr int DT = decltype(d)::value;

@@ -429,13 +429,13 @@ __device__ __forceinline__ void forget_kept(KeptUnit<RT, STORED> &k) {
 // them in its registers; the next row's tensors are on their way while a row
 // is worked on.  A workgroup's teams join their sums in LDS, in order.
 template <int DT, int RT, int U, uint32_t SUB, bool STORED, bool STREAM, bool WHOLE>
-__global__ __launch_bounds__(kMaxThreads) void norm_grad_kernel(GradArgs a) {
+__device__ __forceinline__ void grad_rows(const GradArgs &a, uint32_t blocks) {
     typedef typename Plain<DT>::type TX;
     typedef typename Plain<RT>::type TR;
     __shared__ float part[2][kMaxWaves];
     __shared__ float sums[U == 1 ? kGradThreads * kUnit : 1];
     const Team<SUB> team(a.team);
-    const uint64_t step = (uint64_t)gridDim.x * team.count;
+    const uint64_t step = (uint64_t)blocks * team.count;
     const TX *dy = static_cast<const TX *>(a.dy);
     const TR *d_sum = static_cast<const TR *>(a.d_sum);
     MaskKey key = {};
@@ -535,6 +535,60 @@ __global__ __launch_bounds__(kMaxThreads) void norm_grad_kernel(GradArgs a) {
     }
 }
 
+template <int DT, int RT, int U, uint32_t SUB, bool STORED, bool STREAM, bool WHOLE>
+__global__ __launch_bounds__(kMaxThreads) void norm_grad_kernel(GradArgs a) {
+    grad_rows<DT, RT, U, SUB, STORED, STREAM, WHOLE>(a, gridDim.x);
+}
+
+// The weight's gradient of 64 columns: 8 lanes side by side hold them, the
+// workgroup's groups of 8 lanes take the rows in turns.
+template <int DT, int RT, bool STORED>
+__device__ __forceinline__ void grad_columns(const GradArgs &a, uint32_t block) {
+    constexpr uint32_t kSide = kOnceColumns / kUnit;
+    __shared__ float sums[kMaxThreads * kUnit];
+    const uint32_t tid = threadIdx.x, groups = blockDim.x / kSide, parts = blockDim.x / kWave;
+    const uint32_t col = (block * kSide + tid % kSide) * kUnit, n = count_before(a.cols, col, kUnit);
+    float dw[8] = {};
+#pragma unroll 4
+    for (uint64_t row = tid / kSide; row < a.rows; row += groups) {
+        float g[8], norm[8];
+        load_unit<DT>(static_cast<const typename Plain<DT>::type *>(a.dy) + row * a.ld_dy + col, n, g);
+        widen_kept<RT, STORED>(a, load_kept<RT, STORED, false>(a, row, col, n), norm);
+        const float rstd = a.rstd[row];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[i] += g[i] * (norm[i] * rstd);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sums[tid * kUnit + i] = dw[i];
+    __syncthreads();
+    // a lane to a column, the waves share the groups; then the waves' sums in order
+    const uint32_t lane = tid % kWave, wave = tid / kWave;
+    float s = 0.0f;
+    for (uint32_t g = wave; g < groups; g += parts) s += sums[g * kOnceColumns + lane];
+    __syncthreads();
+    sums[tid] = s;
+    __syncthreads();
+    const uint32_t at = block * kOnceColumns + lane;
+    if (wave || at >= a.cols) return;
+    for (uint32_t p = 1; p < parts; ++p) s += sums[p * kWave + lane];
+    with_dtype(a.d_weight_kind, [&](auto d) {
+        typedef typename Plain<decltype(d)::value>::type T;
+        T *out = static_cast<T *>(a.d_weight) + at;
+        if (a.accumulate) s += widen(*out);
+        *out = (T)s;
+    });
+}
+
+// Few rows in one launch: some workgroups take rows, the others columns, which
+// need nothing of each other: the weight's gradient reads dy and the sum again,
+// but has no partial sums, and the call no second launch and no workspace (128
+// x 2048 f16 with the host's share: 15.7 us, in one launch 11).
+template <int DT, int RT, bool STORED>
+__global__ __launch_bounds__(kMaxThreads) void norm_grad_once_kernel(GradArgs a) {
+    if (blockIdx.x < a.row_blocks) grad_rows<DT, RT, 1, kWave, STORED, false, false>(a, a.row_blocks);
+    else grad_columns<DT, RT, STORED>(a, blockIdx.x - a.row_blocks);
+}
+
 // Rows of more units than a workgroup's registers hold, read twice.
 template <int DT, int RT, bool STORED>
 __global__ __launch_bounds__(kMaxThreads) void norm_grad_long_kernel(GradArgs a) {
@@ -632,6 +686,10 @@ template <int DT, int RT, bool STORED>
 void launch_grad(const GradArgs &a, const GradPlan &p, hipStream_t stream) {
     auto launch = [&](auto k, dim3 grid, uint32_t threads) { hipLaunchKernelGGL(k, grid, dim3(threads), 0, stream, a); };
     const dim3 grid(p.blocks);
+    if (p.once) {
+        launch(norm_grad_once_kernel<DT, RT, STORED>, grid, p.threads);
+        return;
+    }
     if (p.per == 0) {
         // before d_x, which may take dy's place
         if (a.partial) launch(norm_weight_kernel<DT, RT, STORED>, dim3(p.column_blocks, p.slices), kColumnThreads);

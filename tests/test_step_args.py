@@ -96,15 +96,20 @@ def test_norm_sizes():
                                 dict(total=None, q=q8(sym=None)), dict(total=None, q=q8(ld=63)), dict(total=None, q=q8(lds=1)),
                                 dict(wd=3), dict(w=3 * A + 2), dict(rstd=None), dict(rstd=4 * A + 2), dict(ds=5 * A + 1),
                                 dict(ldds=63), dict(ldr=63), dict(dres=6 * A + 1), dict(dx=7 * A + 1), dict(ldx=63),
-                                dict(dw=8 * A + 2), dict(dwd=3), dict(ws=None), dict(ws=9 * A + 8), dict(dres=5 * A, ldr=65),
+                                dict(dw=8 * A + 2), dict(dwd=3), dict(dres=5 * A, ldr=65),
                                 dict(dx=A, ldx=65)] + [dict(m=m) for m in BAD_MASKS])
 def test_norm_backward_refuses(kw):
     assert back(**kw) == BAD
 
 
 def test_norm_backward_sizes():
-    need = pc.pc_rmsnorm_backward_workspace_bytes(4, 64)
-    assert need > 0 and back(wsb=need - 1) == SMALL
+    # few rows take one launch and no room; more of them, or long ones, need it for partial sums
+    assert pc.pc_rmsnorm_backward_workspace_bytes(4, 64) == 0 and pc.pc_rmsnorm_backward_workspace_bytes(512, 4096) == 0
+    for rows, cols in ((513, 64), (512, 4104), (4, 8200)):
+        need = pc.pc_rmsnorm_backward_workspace_bytes(rows, cols)
+        wide = dict(rows=rows, cols=cols, ld=cols, lds=cols, ldds=cols, ldr=cols, ldx=cols)
+        assert need > 0 and back(wsb=need - 1, **wide) == SMALL
+        assert back(ws=None, **wide) == BAD and back(ws=9 * A + 8, **wide) == BAD
     assert pc.pc_rmsnorm_backward_workspace_bytes(0, 64) == 0 and pc.pc_rmsnorm_backward_workspace_bytes(4, 0) == 0
     assert pc.pc_rmsnorm_backward_workspace_bytes(1 << 40, 64) == 0
     nothing = dict(dy=None, total=None, w=None, rstd=None, ds=None, dres=None, dx=None, ws=None, wsb=0)
