@@ -162,9 +162,19 @@ __device__ __forceinline__ void forget(V &v) { asm volatile("" : "+v"(v)); }
 // r = (mean + eps)^-1/2.  Squares are summed in 64 bits, where those of all
 // 32-bit numbers fit; a vector instruction takes as long as in 32 bits.  The
 // hardware's estimate has 23 bits, which a Newton step doubles.
-__device__ __forceinline__ float rstd_of(const NormArgs &a, double squares) {
+__device__ __forceinline__ double rstd_of(const NormArgs &a, double squares) {
     const double m = squares * a.per_col + a.eps, r = __builtin_amdgcn_rsq(m);
-    return m == __builtin_inf() ? 0.0f : (float)(r * (1.5 - 0.5 * m * r * r));
+    return m == __builtin_inf() ? 0.0 : r * (1.5 - 0.5 * m * r * r);
+}
+
+// A number as 32 bits hold it, with an odd last bit where they do not hold all
+// of it: rounding that to fewer bits rounds the number itself.
+__device__ __forceinline__ float rounded_to_odd(double v) {
+    const float s = (float)v;
+    const double rest = v - (double)s;
+    uint32_t u = as_u32(s);
+    if (rest != 0.0 && !(u & 1) && s != 0.0f && (u & 0x7F800000u) != 0x7F800000u) u += (rest > 0.0) == (s > 0.0f) ? 1 : -1;
+    return as_f32(u);
 }
 
 template <int DT>
@@ -207,18 +217,32 @@ __device__ __forceinline__ RawUnit<RT> block_sum(const NormArgs &a, const MaskKe
     return to_raw<RT>(h);
 }
 
-template <bool COUNT>
-__device__ __forceinline__ void norm_unit(const NormArgs &a, uint64_t row, uint32_t col, uint32_t n, float rstd,
-                                          const float w[8], const float h[8], uint32_t *bins) {
+// `again` forms the unit's h and weights once more: they are not kept for the
+// few units that need them.
+template <bool COUNT, class AGAIN>
+__device__ __forceinline__ void norm_unit(const NormArgs &a, uint64_t row, uint32_t col, uint32_t n, double rstd,
+                                          const float w[8], const float h[8], uint32_t *bins, AGAIN &&again) {
     float y[8];
+    const float r = (float)rstd;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = h[i] * rstd * w[i];
+    for (int i = 0; i < 8; ++i) y[i] = h[i] * r * w[i];
     if (a.y && !a.y_stored && n) store_any(a.y_kind, a.y, row * a.ld_y + col, n, y);
     if (!a.sym) return;
     auto store = [&](auto f) {
         constexpr int FMT = decltype(f)::value;
+        // y is off by 3.1 2^-24 at most; where that could change what is stored (one unit of
+        // a wave in 150 or so), the wave forms it again in 64 bits, so that nothing but
+        // the rounding to 8 bits shows
         uint32_t code;
-        const u32x2 s = to_stored<FMT>(y, code);
+        bool unsure;
+        u32x2 s = to_stored<FMT, true>(y, code, &unsure);
+        if (__ballot(unsure)) {
+            float h2[8], w2[8];
+            again(h2, w2);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = rounded_to_odd((double)h2[i] * rstd * (double)w2[i]);
+            s = to_stored<FMT>(y, code);
+        }
         if (n) {
             store_symbols(a.sym + row * a.cols + col, n, s);
             if (col % kGroup == 0) a.scale[row * a.groups + col / kGroup] = (uint8_t)code;
@@ -299,36 +323,41 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a) {
             }
             return s;
         };
-        auto tail = [&](uint32_t base, float rstd) {
+        auto tail = [&](uint32_t base, double rstd) {
 #pragma unroll
             for (int j = 0; j < U; ++j) {
                 const uint32_t col = column(base, j), n = places<WHOLE>(cols, col);
                 float w[8], v[8];
-                if (a.weight) {
-                    widen_any(a.weight_kind, load_any(a.weight_kind, a.weight, col, n), w);
-                } else {
+                auto form = [&](float v[8], float w[8]) {
+                    uint32_t at = col;
+                    forget(at);
+                    if (a.weight) {
+                        widen_any(a.weight_kind, load_any(a.weight_kind, a.weight, at, n), w);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) w[i] = 1.0f;
-                }
-                forget(h[j].w[0]);
-                if constexpr (RT == PC_F32) forget(h[j].w[1]);
-                widen_unit<RT>(h[j], v);
-                norm_unit<COUNT>(a, row, col, n, rstd, w, v, bins);
+                        for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+                    }
+                    forget(h[j].w[0]);
+                    if constexpr (RT == PC_F32) forget(h[j].w[1]);
+                    widen_unit<RT>(h[j], v);
+                };
+                form(v, w);
+                norm_unit<COUNT>(a, row, col, n, rstd, w, v, bins, form);
                 if constexpr (U > 1) __builtin_amdgcn_sched_barrier(0);  // one unit's registers at a time
             }
         };
         if constexpr (!LONG) {
             const double own = head(0, sum != nullptr);
-            const float rstd = rstd_of(a, team_sum(team, own, part[turn]));
-            if (team.at == 0 && cols && a.rstd) a.rstd[row] = rstd;
+            const double rstd = rstd_of(a, team_sum(team, own, part[turn]));
+            if (team.at == 0 && cols && a.rstd) a.rstd[row] = (float)rstd;
             tail(0, rstd);
         } else {
             // the last units' group of 4 lanes stays whole
             const uint32_t units = (a.cols + kGroup - 1) / kGroup * kUnitsPerGroup;
             double own = 0.0;
             for (uint32_t base = 0; base < units; base += U * team.lanes) own += head(base, sum != nullptr);
-            const float rstd = rstd_of(a, team_sum(team, own, part[turn]));
-            if (team.at == 0 && cols && a.rstd) a.rstd[row] = rstd;
+            const double rstd = rstd_of(a, team_sum(team, own, part[turn]));
+            if (team.at == 0 && cols && a.rstd) a.rstd[row] = (float)rstd;
             for (uint32_t base = 0; base < units; base += U * team.lanes) {
                 if (sum) {  // the sum may have taken an input's place: it is read back by the lanes that wrote it
 #pragma unroll

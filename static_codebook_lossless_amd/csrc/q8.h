@@ -251,9 +251,11 @@ __device__ __forceinline__ u32x2 with_nan(u32x2 w, uint32_t bad) {
 
 // The symbols of the lane's 8 values and their group's scale code.  The four
 // lanes that hold a group take part together; v is changed where it holds
-// infinities and NaN, which take no part in the scale.
-template <int FMT>
-__device__ __forceinline__ u32x2 to_stored(float v[8], uint32_t &code) {
+// infinities and NaN, which take no part in the scale.  UNSURE: the values may
+// each be off by a relative 2^-22, and `unsure` tells whether that could change
+// a symbol of the lane or the code.
+template <int FMT, bool UNSURE = false>
+__device__ __forceinline__ u32x2 to_stored(float v[8], uint32_t &code, bool *unsure = nullptr) {
     uint32_t top = 0, bad = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = max(top, as_u32(v[i]) & 0x7FFFFFFFu);
@@ -270,8 +272,17 @@ __device__ __forceinline__ u32x2 to_stored(float v[8], uint32_t &code) {
             }
         }
     }
-    code = code_for<FMT>(quad_max(top));
-    u32x2 w = to_symbols<FMT>(v, as_f32((254 - code) << 23));
+    top = quad_max(top);
+    code = code_for<FMT>(top);
+    const uint32_t inv = (254 - code) << 23;
+    u32x2 w;
+    if constexpr (UNSURE) {  // 2^-21 to either side, of which the products' rounding takes a part
+        const u32x2 up = to_symbols<FMT>(v, as_f32(inv + 4));
+        w = to_symbols<FMT>(v, as_f32(inv - 8));
+        *unsure = w[0] != up[0] || w[1] != up[1] || code_for<FMT>(top + 4) != code_for<FMT>(max(top, 4u) - 4);
+    } else {
+        w = to_symbols<FMT>(v, as_f32(inv));
+    }
     if (bad) w = with_nan<FMT>(w, bad);
     return w;
 }

@@ -160,7 +160,7 @@ def test_norm_weight_gradient_without_rows():
 # streamed inputs, rows read twice, several rows of a team
 LAUNCHES = [(5, 128), (5, 136), (70, 256), (70, 264), (5, 512), (5, 520), (1300, 64), (1300, 250), (9, 8192), (9, 8200),
             (3, 16384), (3, 16392), (3, 16390), (3, 32768), (3, 32776), (9000, 72), (1100, 512), (700, 520), (300, 1003),
-            (512, 4096), (513, 4096), (512, 4104), (512, 40), (513, 40), (1, 65), (37, 8192)]
+            (512, 8192), (513, 4096), (512, 4104), (512, 40), (513, 40), (1, 65), (37, 8192)]
 
 
 @pytest.mark.parametrize("dtype,res", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f32")])

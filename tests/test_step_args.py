@@ -104,8 +104,8 @@ def test_norm_backward_refuses(kw):
 
 def test_norm_backward_sizes():
     # few rows take one launch and no room; more of them, or long ones, need it for partial sums
-    assert pc.pc_rmsnorm_backward_workspace_bytes(4, 64) == 0 and pc.pc_rmsnorm_backward_workspace_bytes(512, 4096) == 0
-    for rows, cols in ((513, 64), (512, 4104), (4, 8200)):
+    assert pc.pc_rmsnorm_backward_workspace_bytes(4, 64) == 0 and pc.pc_rmsnorm_backward_workspace_bytes(512, 8192) == 0
+    for rows, cols in ((513, 64), (512, 8200), (4, 8200)):
         need = pc.pc_rmsnorm_backward_workspace_bytes(rows, cols)
         wide = dict(rows=rows, cols=cols, ld=cols, lds=cols, ldds=cols, ldr=cols, ldx=cols)
         assert need > 0 and back(wsb=need - 1, **wide) == SMALL
