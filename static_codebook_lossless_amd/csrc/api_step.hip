@@ -118,7 +118,7 @@ pc_status pc_rmsnorm_backward(const void *d_dy, int dtype, size_t rows, size_t c
     if (stored_sum && (stored_sum->rows != rows || stored_sum->cols != cols || !is_format(stored_sum->format)))
         return PC_ERR_INVALID_ARG;
     if (cols == 0 || (rows == 0 && (accumulate || !d_dweight))) return PC_OK;
-    if (d_dweight && !plain_ok(d_dweight, dweight_dtype, cols, cols)) return PC_ERR_INVALID_ARG;
+    if (d_dweight && (d_dweight == d_weight || !plain_ok(d_dweight, dweight_dtype, cols, cols))) return PC_ERR_INVALID_ARG;
     if (rows) {
         if (!plain_ok(d_dy, dtype, cols, ld_dy) || (d_weight && !plain_ok(d_weight, weight_dtype, cols, cols)) ||
             !d_rstd || !aligned(d_rstd, 4))

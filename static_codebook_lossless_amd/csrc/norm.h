@@ -56,6 +56,7 @@ struct GradPlan {
     uint32_t parts;                       // rows of partial sums
     uint32_t column_blocks, slices;       // of the long rows' weight gradient
     bool whole, streams, once;            // once: blocks for rows and for columns in one launch
+    bool columns_first;                   // of these, the columns' in a launch before: the rows' write what they read
 };
 
 

@@ -194,9 +194,9 @@ hipError_t launch_rmsnorm_backward(const RmsNormGrad &c, hipStream_t stream) {
     const uint64_t kept = c.stored ? 1 : size_of(c.sum_dtype), d_sum = c.d_sum ? size_of(c.sum_dtype) : 0;
     GradArgs a = {};
     const bool once = c.d_weight && c.rows && once_fits(c.rows, c.cols);
-    const GradPlan p = once ? plan_once(c.rows, c.cols, a.row_blocks)
-                            : plan_grad(c.rows, c.cols, c.sum_dtype == PC_F32,
-                                        c.rows * c.cols * (size_of(c.dtype) + kept + d_sum));
+    GradPlan p = once ? plan_once(c.rows, c.cols, a.row_blocks)
+                      : plan_grad(c.rows, c.cols, c.sum_dtype == PC_F32,
+                                  c.rows * c.cols * (size_of(c.dtype) + kept + d_sum));
     a.dy = c.dy;
     a.sum = c.sum;
     a.ld_sum = c.ld_sum;
@@ -225,6 +225,7 @@ hipError_t launch_rmsnorm_backward(const RmsNormGrad &c, hipStream_t stream) {
     a.ld_partial = partial_width(c.cols);
     a.cols = (uint32_t)c.cols;
     a.team = p.team;
+    p.columns_first = (c.d_x && c.d_x == c.dy) || (c.d_res && (c.d_res == c.sum || c.d_res == c.dy));
     a.per_col = (float)(1.0 / (double)c.cols);
     a.mask = mask_arg(c.mask);
     if (c.rows) {

@@ -716,7 +716,15 @@ void launch_grad(const GradArgs &a, const GradPlan &p, hipStream_t stream) {
     auto launch = [&](auto k, dim3 grid, uint32_t threads) { hipLaunchKernelGGL(k, grid, dim3(threads), 0, stream, a); };
     const dim3 grid(p.blocks);
     if (p.once) {
-        launch(norm_grad_once_kernel<DT, RT, STORED>, grid, p.threads);
+        if (!p.columns_first) {
+            launch(norm_grad_once_kernel<DT, RT, STORED>, grid, p.threads);
+            return;
+        }
+        const auto k = norm_grad_once_kernel<DT, RT, STORED>;
+        GradArgs columns = a;
+        columns.row_blocks = 0;
+        hipLaunchKernelGGL(k, dim3(p.blocks - a.row_blocks), dim3(p.threads), 0, stream, columns);
+        launch(k, dim3(a.row_blocks), p.threads);
         return;
     }
     if (p.per == 0) {

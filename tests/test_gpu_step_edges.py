@@ -571,7 +571,7 @@ def test_binding_refuses():
 
 # -- forms that only the C entries have ------------------------------------------------
 
-@pytest.mark.parametrize("rows,cols", [(70, 264), (9, 8200), (5, 8191), (4, 33000), (3, 40001)])
+@pytest.mark.parametrize("rows,cols", [(70, 264), (512, 8192), (400, 5001), (600, 520), (9, 8200), (5, 8191), (4, 33000), (3, 40001)])
 def test_norm_backward_in_place(rows, cols):
     """The residual's gradient over the one that comes in, x's over y's."""
     lib = pc._lib.lib

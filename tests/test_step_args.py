@@ -96,7 +96,7 @@ def test_norm_sizes():
                                 dict(total=None, q=q8(sym=None)), dict(total=None, q=q8(ld=63)), dict(total=None, q=q8(lds=1)),
                                 dict(wd=3), dict(w=3 * A + 2), dict(rstd=None), dict(rstd=4 * A + 2), dict(ds=5 * A + 1),
                                 dict(ldds=63), dict(ldr=63), dict(dres=6 * A + 1), dict(dx=7 * A + 1), dict(ldx=63),
-                                dict(dw=8 * A + 2), dict(dwd=3), dict(dres=5 * A, ldr=65),
+                                dict(dw=8 * A + 2), dict(dwd=3), dict(dw=3 * A), dict(dres=5 * A, ldr=65),
                                 dict(dx=A, ldx=65)] + [dict(m=m) for m in BAD_MASKS])
 def test_norm_backward_refuses(kw):
     assert back(**kw) == BAD
