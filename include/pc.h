@@ -45,7 +45,10 @@
  *   int8 symbols with one power-of-two scale for every 32 columns (the
  *   symbols are what pc_encode codes and pc_histogram counts), and uses the
  *   symbols, as pc_decode gives them back, in the backward pass and as an
- *   embedding table.
+ *   embedding table.  The last part has what stands between the products of
+ *   such a step: the norm of a residual block, which stores its output, dropout
+ *   from a counter, and the loss (log probabilities of given tokens, the
+ *   entropy and the logits' gradient).
  *
  * Memory
  *   The library never allocates.  Every buffer belongs to the caller; device
@@ -532,7 +535,7 @@ pc_status pc_dropout(const void *d_x, int dtype, size_t rows, size_t cols, size_
  *            values in its place, as pc_q8_load gives them (needs d_sym).
  *   d_rstd   NULL, or receives rows f32.
  * Squares are summed in 64 bits.  A row that holds an infinity has rstd 0, one
- * that holds NaN has rstd NaN.  cols is below 2^31.
+ * that holds NaN has rstd NaN.  cols is below 2^31; cols == 0 writes nothing, rstd neither.
  */
 pc_status pc_rmsnorm_store(const void *d_x, int dtype, size_t rows, size_t cols, size_t ldx, const void *d_res,
                            int sum_dtype, size_t ld_res, const pc_mask *mask, const void *d_weight, int weight_dtype,
