@@ -529,8 +529,8 @@ pc_status pc_dropout(const void *d_x, int dtype, size_t rows, size_t cols, size_
  *   eps      positive and finite.
  *   d_sum    NULL, or receives h; may be d_res, or d_x where the types agree (same ld).  NULL without d_res and mask (h is x).
  *   d_sym, d_scale  NULL, or receive y as pc_q8_store would store it, dense;
- *            d_counts as there (NULL without d_sym).  y goes into the stored
- *            form from 32 bits, without an earlier rounding.
+ *            d_counts as there (NULL without d_sym).  What is stored is y
+ *            from h in 64 bits, rounded once.
  *   d_y      NULL, or receives y rounded to y_dtype; where y_stored, the stored
  *            values in its place, as pc_q8_load gives them (needs d_sym).
  *   d_rstd   NULL, or receives rows f32.
