@@ -369,14 +369,15 @@ __device__ __forceinline__ void finish(const Args &a, uint64_t row, Soft soft, u
     }
 }
 
-constexpr uint32_t kRowThreads = 256;
+constexpr uint32_t kRowThreads = 256, kWideThreads = 512;
 
 constexpr uint32_t kFirst = 2 * kWave;
 
+template <uint32_t THREADS>
 struct TopArea {
-    uint64_t lists[kRowThreads], pools[kRowThreads / kWave * kPool], first[kFirst];
-    uint32_t keys[kRowThreads], found;
-    uint8_t strips[kRowThreads];
+    uint64_t lists[THREADS], pools[THREADS / kWave * kPool], first[kFirst];
+    uint32_t keys[3][THREADS], found;  // keys: a step each for up to 8 waves
+    uint8_t strips[THREADS];
 };
 
 __device__ __forceinline__ uint32_t lanes_before(uint64_t mask) {
@@ -422,27 +423,29 @@ __device__ __forceinline__ uint64_t largest_in_order(const Args &a, const typena
 //
 // The `top`th largest of these lanes' largest is at most the `top`th of all
 // elements, and hardly less: the largest elements mostly lie in strips of their
-// own.  Strips whose largest is below it hold none of them; of the few others
-// the wave reads all units again, side by side, and takes what is not below the
-// bound: with 256 strips little more than `top` elements, which one wave sorts.
-// Where ties make them more than 128 (a masked stretch is equal throughout),
-// the waves go over their strips in order.  So the pass over the row does
-// nothing for the alternatives; comparing every element with the least one kept
-// so far doubles its work (2048 x 32000 bf16, 20 of them: 66 us, without them 31).
-template <int DT>
+// own.  The waves join their lists two by two, all of them in each step, so three
+// steps give it to eight waves.  Strips whose largest is below it hold none of
+// them; of the few others the wave reads all units again, side by side, and
+// takes what is not below the bound: with 256 strips little more than `top`
+// elements, which one wave sorts.  Where ties make them more than 128 (a masked
+// stretch is equal throughout), the waves go over their strips in order.  So
+// the pass over the row does nothing for the alternatives; comparing every
+// element with the least one kept so far doubles its work (2048 x 32000 bf16, 20
+// of them: 66 us, without them 31).
+template <int DT, class AREA>
 __device__ __forceinline__ uint64_t largest_elements(const Args &a, const typename Plain<DT>::type *x, uint32_t begin,
-                                                     uint32_t end, uint32_t key, TopArea &area) {
+                                                     uint32_t end, uint32_t key, AREA &area) {
     constexpr uint32_t N = kPer<DT>;
     const uint32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave), threads = blockDim.x;
     const uint32_t nothing = key_of(-__builtin_inff());
     uint32_t best_keys = a.top == 1 ? wave_max(key) : sorted(key);
     if (threads > kWave) {
-        area.keys[threadIdx.x] = best_keys;
         if (threadIdx.x == 0) area.found = 0;
-        __syncthreads();
-        for (uint32_t w = 0; w < threads / kWave; ++w) {
-            const uint32_t other = area.keys[w * kWave + lane];
-            if (w != wave) best_keys = a.top == 1 ? max(best_keys, other) : merged(best_keys, other);
+        for (uint32_t half = 1, level = 0; half < threads / kWave; half *= 2, ++level) {
+            area.keys[level][threadIdx.x] = best_keys;
+            __syncthreads();
+            const uint32_t other = area.keys[level][(wave ^ half) * kWave + lane];
+            best_keys = a.top == 1 ? max(best_keys, other) : merged(best_keys, other);
         }
     }
     const uint32_t bound = max(1u, from_lane(best_keys, a.top - 1));  // 0: fewer lanes than that have read any
@@ -517,15 +520,15 @@ __device__ __forceinline__ uint64_t largest_elements(const Args &a, const typena
 // A workgroup takes a row, or one of `splits` stretches of it: a batch of
 // elements gives a maximum first, for which the sums so far are moved if it is
 // a new one, then an exponential and two sums an element.  4096 x 128000 bf16:
-// 172 us, 6.1 TB/s, with vector work in all of the cycles; 511 x 32001 f32 with 4
-// tokens and 5 alternatives: 19-20 us, two workgroups to a CU, 15 without the
+// 170 us, 6.2 TB/s, with vector work in all of the cycles; 511 x 32001 f32 with 4
+// tokens and 5 alternatives: 18 us, two workgroups to a CU, 13 without the
 // alternatives; 1 x 128000 with 20: 9.4 us in 31 stretches, and 4.8 for the join.
-template <int DT, bool TOP, bool STREAM>
-__global__ __launch_bounds__(kRowThreads, TOP ? 6 : 8) void rows_kernel(Args a) {
+template <int DT, bool TOP, bool STREAM, uint32_t THREADS>
+__global__ __launch_bounds__(THREADS, TOP ? 6 : 8) void rows_kernel(Args a) {
     typedef typename Plain<DT>::type T;
     constexpr uint32_t N = kPer<DT>;
     __shared__ Soft softs[kMaxWaves];
-    __shared__ std::conditional_t<TOP, TopArea, char> area;
+    __shared__ std::conditional_t<TOP, TopArea<THREADS>, char> area;
     const uint32_t tid = threadIdx.x, threads = blockDim.x, step = threads * kVecs;
     const float c = a.scale * kLog2E;
     const uint64_t total = a.rows * a.splits;
@@ -754,6 +757,16 @@ bool streams(uint64_t rows, uint64_t vocab, int dtype) { return rows * vocab * (
 
 struct Plan { uint32_t threads, splits, per_split; };
 
+// Stretches of so many 16-byte units get 512 lanes: where that leaves no more than
+// two workgroups to a CU, for the loads on their way, and longer ones always, for
+// their alternatives, whose strips are then half as long.  With 256 lanes and 512:
+// 511 x 32001 f32 without alternatives 15.3 and 13.4 us, with 20 23.5 and 19.4;
+// 512 x 128000 bf16 37.9 and 28.4, 50.1 and 36.3; 256 x 50257 bf16 (2 x 3142 units)
+// 13.9 and 14.0, 21.9 and 21.7.  2048 x 128000 f32 159 and 157, 261 and 199; 4096 x
+// 128000 bf16 170 and 164, with 5 189 and 194, with 20 248 and 218; 1024 x 32000 f32
+// 26.4 and 27.0, 36.6 and 39.3.  1024 lanes: 222 for 2048 x 128000 f32 with 20.
+constexpr uint32_t kWideFrom = 4096, kAlwaysWideFrom = 12288;
+
 // A wave to a row where the rows fill the chip with waves and are short, or
 // hold no more than a wave's loads (8192 x 4000 bf16: 18 us, with four waves
 // 39; 2048 x 32000: 31 and 28).  Few rows are split, down to what a workgroup
@@ -771,6 +784,7 @@ Plan plan_rows(uint64_t rows, uint64_t vocab, int dtype) {
         p.per_split = (units + wanted - 1) / wanted;
         p.splits = (units + p.per_split - 1) / p.per_split;
     }
+    if (p.per_split >= (rows * p.splits <= 512 ? kWideFrom : kAlwaysWideFrom)) p.threads = kWideThreads;
     return p;
 }
 
@@ -815,10 +829,18 @@ hipError_t launch_logprobs(const LogProbs &c, hipStream_t stream) {
             hipLaunchKernelGGL(k, g, dim3(threads), 0, stream, a);
         };
         const bool stream_in = streams(c.rows, c.vocab, c.dtype);
-        if (c.top && stream_in) launch(rows_kernel<DT, true, true>, grid, p.threads);
-        else if (c.top) launch(rows_kernel<DT, true, false>, grid, p.threads);
-        else if (stream_in) launch(rows_kernel<DT, false, true>, grid, p.threads);
-        else launch(rows_kernel<DT, false, false>, grid, p.threads);
+        auto rows_of = [&](auto t) {
+            constexpr uint32_t T = decltype(t)::value;
+            if (c.top && stream_in) launch(rows_kernel<DT, true, true, T>, grid, p.threads);
+            else if (c.top) launch(rows_kernel<DT, true, false, T>, grid, p.threads);
+            else if (stream_in) launch(rows_kernel<DT, false, true, T>, grid, p.threads);
+            else launch(rows_kernel<DT, false, false, T>, grid, p.threads);
+        };
+        // an area for a wave's own lanes alone leaves LDS for 24 of them (8192 x 1000 with 20
+        // alternatives: 18 us, with that of 256 lanes 24)
+        if (p.threads == kWave) rows_of(std::integral_constant<uint32_t, kWave>());
+        else if (p.threads == kWideThreads) rows_of(std::integral_constant<uint32_t, kWideThreads>());
+        else rows_of(std::integral_constant<uint32_t, kRowThreads>());
         if (p.splits > 1) {
             const dim3 rows((uint32_t)c.rows);  // 256 at most
             if (c.top) launch(join_kernel<DT, true>, rows, kMaxThreads);

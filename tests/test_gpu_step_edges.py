@@ -314,7 +314,8 @@ def test_nan_and_infinity_stay_visible(vocab):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("rows,vocab", [(2, 64), (1, 70), (3, 2048), (2, 9000), (1, 131072), (300, 5000), (4500, 600)])
+@pytest.mark.parametrize("rows,vocab", [(2, 64), (1, 70), (3, 2048), (2, 9000), (1, 131072), (300, 5000), (4500, 600),
+                                        (257, 33000)])
 def test_equal_logits_go_by_index(dtype, rows, vocab):
     """Ties: constant rows, rows of few values, both zeros, ascending and descending ones."""
     rng = np.random.default_rng(32)
@@ -425,7 +426,9 @@ def test_logits_of_other_shapes_and_strides():
 @pytest.mark.parametrize("dtype,rows,vocab", [("bf16", 4096, 2048), ("bf16", 4095, 2048), ("bf16", 4096, 32776),
                                               ("bf16", 257, 33000), ("bf16", 256, 16384), ("bf16", 256, 16376),
                                               ("f32", 255, 8192), ("f32", 255, 8188), ("bf16", 4200, 16000),
-                                              ("f32", 600, 60001), ("f16", 20, 260000)])
+                                              ("f32", 600, 60001), ("f16", 20, 260000), ("f32", 512, 16384),
+                                              ("f32", 512, 16380), ("f32", 513, 49148), ("bf16", 513, 98304),
+                                              ("bf16", 100, 170000), ("bf16", 2, 5600000)])
 def test_logprobs_where_launches_change(dtype, rows, vocab):
     rng = torch.Generator(device=DEV).manual_seed(6)
     x = (torch.randn(rows, vocab, generator=rng, device=DEV) * 3).to(DT[dtype])
