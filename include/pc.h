@@ -531,8 +531,9 @@ pc_status pc_dropout(const void *d_x, int dtype, size_t rows, size_t cols, size_
  *   d_sym, d_scale  NULL, or receive y as pc_q8_store would store it, dense;
  *            d_counts as there (NULL without d_sym).  What is stored is y
  *            from h in 64 bits, rounded once.
- *   d_y      NULL, or receives y rounded to y_dtype; where y_stored, the stored
- *            values in its place, as pc_q8_load gives them (needs d_sym).
+ *   d_y      NULL, or receives y rounded to y_dtype (from 32 bits, which have y
+ *            to 3.1 2^-24 of it or 2^-126); where y_stored, the stored values in
+ *            its place, as pc_q8_load gives them (needs d_sym).
  *   d_rstd   NULL, or receives rows f32.
  * Squares are summed in 64 bits.  A row that holds an infinity has rstd 0, one
  * that holds NaN has rstd NaN.  cols is below 2^31; cols == 0 writes nothing, rstd neither.

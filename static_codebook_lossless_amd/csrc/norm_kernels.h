@@ -219,13 +219,37 @@ __device__ __forceinline__ RawUnit<RT> block_sum(const NormArgs &a, const MaskKe
 
 // `again` forms the unit's h and weights once more: they are not kept for the
 // few units that need them.
-template <bool COUNT, class AGAIN>
+//
+// y is (h r) w in 32 bits, off by 3.1 2^-24, as long as r and h r are normal
+// numbers.  r of a row above 2^126 has fewer digits, and a small h in a row of
+// large ones leaves h r below 2^-126, off by 2^-150, and y by that times the
+// weight (FAINT: no sum in f16 has either).  Units where it could be seen are
+// formed in 64 bits: from a weight of 2^24 on, which makes it 2^-126, and for
+// what is stored from one of 1 on where the group's scale is small (at those
+// above kFaintCode it is at most 2^-34 of the scale, which `unsure` covers
+// beside the 3.1 2^-24).
+constexpr float kNormal = 0x1p-126f, kFaintWeight = 0x1p24f;
+constexpr uint32_t kFaintCode = 34;
+
+template <bool COUNT, bool FAINT, class AGAIN>
 __device__ __forceinline__ void norm_unit(const NormArgs &a, uint64_t row, uint32_t col, uint32_t n, double rstd,
                                           const float w[8], const float h[8], uint32_t *bins, AGAIN &&again) {
     float y[8];
     const float r = (float)rstd;
+    float heavy = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = h[i] * r * w[i];
+    for (int i = 0; i < 8; ++i) {
+        y[i] = h[i] * r * w[i];
+        heavy = fmaxf(heavy, fabsf(w[i]));
+    }
+    const bool faint = FAINT && (heavy > kFaintWeight || r < kNormal), above_1 = FAINT && heavy > 1.0f;
+    auto precise = [&](auto round) {
+        float h2[8], w2[8];
+        again(h2, w2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = round((double)h2[i] * rstd * (double)w2[i]);
+    };
+    if (faint && a.y && !a.y_stored) precise([](double v) { return (float)v; });
     if (a.y && !a.y_stored && n) store_any(a.y_kind, a.y, row * a.ld_y + col, n, y);
     if (!a.sym) return;
     auto store = [&](auto f) {
@@ -236,11 +260,9 @@ __device__ __forceinline__ void norm_unit(const NormArgs &a, uint64_t row, uint3
         uint32_t code;
         bool unsure;
         u32x2 s = to_stored<FMT, true>(y, code, &unsure);
+        unsure |= faint || (above_1 && code <= kFaintCode);
         if (__ballot(unsure)) {
-            float h2[8], w2[8];
-            again(h2, w2);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = rounded_to_odd((double)h2[i] * rstd * (double)w2[i]);
+            precise(rounded_to_odd);
             s = to_stored<FMT>(y, code);
         }
         if (n) {
@@ -347,7 +369,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a) {
                     widen_unit<RT>(h[j], v);
                 };
                 form(v, w);
-                norm_unit<COUNT>(a, row, col, n, rstd, w, v, bins, form);
+                norm_unit<COUNT, RT != PC_F16>(a, row, col, n, rstd, w, v, bins, form);
                 if constexpr (U > 1) __builtin_amdgcn_sched_barrier(0);  // one unit's registers at a time
             }
         };
