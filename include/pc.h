@@ -530,7 +530,7 @@ pc_status pc_dropout(const void *d_x, int dtype, size_t rows, size_t cols, size_
  *   d_sum    NULL, or receives h; may be d_res, or d_x where the types agree (same ld).  NULL without d_res and mask (h is x).
  *   d_sym, d_scale  NULL, or receive y as pc_q8_store would store it, dense;
  *            d_counts as there (NULL without d_sym).  What is stored is y
- *            from h in 64 bits, rounded once.
+ *            from h in 64 bits, rounded once; what f32 cannot hold counts as infinite.
  *   d_y      NULL, or receives y rounded to y_dtype (from 32 bits, which have y
  *            to 3.1 2^-24 of it or 2^-126); where y_stored, the stored values in
  *            its place, as pc_q8_load gives them (needs d_sym).

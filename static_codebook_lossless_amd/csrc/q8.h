@@ -253,12 +253,14 @@ __device__ __forceinline__ u32x2 with_nan(u32x2 w, uint32_t bad) {
 // lanes that hold a group take part together; v is changed where it holds
 // infinities and NaN, which take no part in the scale.  UNSURE: the values may
 // each be off by a relative 2^-22, and `unsure` tells whether that could change
-// a symbol of the lane or the code.
+// a symbol of the lane or the code, or make an infinity of the largest numbers
+// or one of these of an infinity.
 template <int FMT, bool UNSURE = false>
 __device__ __forceinline__ u32x2 to_stored(float v[8], uint32_t &code, bool *unsure = nullptr) {
     uint32_t top = 0, bad = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = max(top, as_u32(v[i]) & 0x7FFFFFFFu);
+    const bool at_end = top >= 0x7F800000u - 8;
     if (top >= 0x7F800000u) {
         top = 0;
 #pragma unroll
@@ -279,7 +281,8 @@ __device__ __forceinline__ u32x2 to_stored(float v[8], uint32_t &code, bool *uns
     if constexpr (UNSURE) {  // 2^-21 to either side, of which the products' rounding takes a part
         const u32x2 up = to_symbols<FMT>(v, as_f32(inv + 4));
         w = to_symbols<FMT>(v, as_f32(inv - 8));
-        *unsure = w[0] != up[0] || w[1] != up[1] || code_for<FMT>(top + 4) != code_for<FMT>(max(top, 4u) - 4);
+        *unsure = at_end || w[0] != up[0] || w[1] != up[1] ||
+                  code_for<FMT>(top + 4) != code_for<FMT>(max(top, 4u) - 4);
     } else {
         w = to_symbols<FMT>(v, as_f32(inv));
     }

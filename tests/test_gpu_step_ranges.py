@@ -1,6 +1,7 @@
-"""The norm where a product of two of its factors leaves the range of 32 bits.
-Tolerances are those of test_gpu_step.py: y has 3.1 u, and the stored form equals
-that of y in 64 bits, byte for byte."""
+"""The norm where a product of two of its factors leaves the range of 32 bits,
+and where its output comes to the end of it.  Tolerances are those of
+test_gpu_step.py: y has 3.1 u, and the stored form equals that of y in 64 bits,
+byte for byte."""
 import numpy as np
 import pytest
 import torch
@@ -70,3 +71,36 @@ def test_reciprocal_roots_below_the_normal_range(dtype):
             y, _ = step.norm(np64(x), np64(w), EPS)
             within(np64(r.y), y, 3.1 * U * np.abs(y))
             check_stored(r.q, y, fmt)
+
+
+END = 2.0 ** 128 - 2.0 ** 103  # from here on 32 bits round to infinity
+
+
+def ends():
+    """(h, weight) of which y in 64 bits rounds to the largest number of 32 bits, and products in 32 bits to infinity, and the reverse."""
+    found = {}
+    for h in 1 + np.arange(1, 40, dtype=np.float32) / 64:
+        rstd = 1 / np.sqrt(np.float64(h) ** 2 / 64 + EPS)
+        first = np.float32(END / (np.float64(h) * rstd))
+        for k in range(-4, 5):
+            w = np.float32(first + k * np.spacing(first))
+            exact = np.float64(h) * rstd * np.float64(w)
+            with np.errstate(over="ignore"):
+                product = np.float32(np.float32(h * np.float32(rstd)) * w)
+            if np.isinf(product) != (exact >= END):
+                found[bool(exact >= END)] = h, w
+    return found
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_stored_outputs_at_the_end_of_the_range(dtype):
+    found = ends()
+    assert set(found) == {False, True}
+    for h, w in found.values():
+        x, weight = torch.zeros(2, 64, device=DEV), torch.ones(64, device=DEV)
+        x[:, 0], weight[0] = float(h), float(w)
+        x = x.to(DT[dtype])
+        for fmt in ("e4m3", "int8"):
+            r = pc.pc_rmsnorm_store(x, weight, format=fmt)
+            y, _ = step.norm(np64(x), np64(weight), EPS)
+            check_stored(r.q, np.where(y >= END, np.inf, y), fmt)
