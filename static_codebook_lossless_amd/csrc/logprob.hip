@@ -625,7 +625,9 @@ __global__ __launch_bounds__(THREADS, TOP ? 6 : 8) void rows_kernel(Args a) {
     }
 }
 
-// The stretches of a row joined: a wave takes every 16th, in order.
+// The stretches of a row joined: a lane takes the sums of one each (there are 512
+// at most, and the launch has lanes for all), with alternatives or without, so
+// these change no sum's order; a wave takes every 16th list, in order.
 template <int DT, bool TOP>
 __global__ __launch_bounds__(kMaxThreads) void join_kernel(Args a) {
     __shared__ Soft softs[kMaxWaves];
@@ -637,8 +639,7 @@ __global__ __launch_bounds__(kMaxThreads) void join_kernel(Args a) {
     if (wave == 0) p = pick<DT>(a, row);
     Soft soft = nothing();
     uint64_t best = 0;
-    for (uint32_t s = wave * kWave + lane; s < a.splits; s += blockDim.x)
-        soft = joined(soft, a.soft[row * a.splits + s], c);
+    if (threadIdx.x < a.splits) soft = joined(soft, a.soft[row * a.splits + threadIdx.x], c);
     soft = wave_soft(soft, c);
     if constexpr (TOP) {
         for (uint32_t s = wave; s < a.splits; s += waves)
@@ -757,6 +758,9 @@ bool streams(uint64_t rows, uint64_t vocab, int dtype) { return rows * vocab * (
 
 struct Plan { uint32_t threads, splits, per_split; };
 
+constexpr uint32_t kMostSplits = 512;  // of all rows together
+static_assert(kMostSplits <= kMaxThreads, "the join has a lane for each");
+
 // Stretches of so many 16-byte units get 512 lanes: where that leaves no more than
 // two workgroups to a CU, for the loads on their way, and longer ones always, for
 // their alternatives, whose strips are then half as long.  With 256 lanes and 512:
@@ -780,7 +784,7 @@ Plan plan_rows(uint64_t rows, uint64_t vocab, int dtype) {
     p.per_split = units;
     const uint32_t least = kRowThreads * kVecs;
     if (rows <= 256 && units >= 2 * least) {
-        const uint32_t wanted = (uint32_t)std::min<uint64_t>(512 / std::max<uint64_t>(rows, 1), units / least);
+        const uint32_t wanted = (uint32_t)std::min<uint64_t>(kMostSplits / std::max<uint64_t>(rows, 1), units / least);
         p.per_split = (units + wanted - 1) / wanted;
         p.splits = (units + p.per_split - 1) / p.per_split;
     }
@@ -844,7 +848,7 @@ hipError_t launch_logprobs(const LogProbs &c, hipStream_t stream) {
         if (p.splits > 1) {
             const dim3 rows((uint32_t)c.rows);  // 256 at most
             if (c.top) launch(join_kernel<DT, true>, rows, kMaxThreads);
-            else launch(join_kernel<DT, false>, rows, kWave);
+            else launch(join_kernel<DT, false>, rows, (p.splits + kWave - 1) / kWave * kWave);
         }
     });
     return hipGetLastError();
