@@ -554,10 +554,11 @@ pc_status pc_rmsnorm_store(const void *d_x, int dtype, size_t rows, size_t cols,
  *   d_rstd   rows f32, as the forward pass gave them.
  *   d_dsum   NULL, or the gradient that reaches h on the residual's way, of sum_dtype.
  *   mask     NULL, or the forward pass's.
- *   d_dres   NULL, or receives d in sum_dtype; may be d_dsum (same ld).
- *   d_dx     NULL, or receives mask(d) in dtype; may be d_dy (same ld).
- *   d_dweight  NULL, or receives cols numbers of dweight_dtype (not d_weight); each is summed in 32
- *            bits in an order that depends on the sizes alone.
+ *   d_dres   NULL, or receives d in sum_dtype.
+ *   d_dx     NULL, or receives mask(d) in dtype.  Each of the two may be one of d_dy, d_sum and
+ *            d_dsum of its type (same ld); no output overlaps an input otherwise, or another output.
+ *   d_dweight  NULL, or receives cols numbers of dweight_dtype (no other argument's memory); each
+ *            is summed in 32 bits in an order that depends on the sizes alone.
  *   d_ws, ws_bytes  scratch of pc_rmsnorm_backward_workspace_bytes (0 for few
  *            rows, then d_ws may be NULL), 16-byte aligned; not needed without d_dweight.
  * rows == 0: d_weight = 0, or stays where accumulate.

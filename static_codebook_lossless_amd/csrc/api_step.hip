@@ -129,9 +129,21 @@ pc_status pc_rmsnorm_backward(const void *d_dy, int dtype, size_t rows, size_t c
             (d_dres && !plain_ok(d_dres, sum_dtype, cols, ld_dres)) ||
             (d_dx && !plain_ok(d_dx, dtype, cols, ld_dx)))
             return PC_ERR_INVALID_ARG;
-        if ((d_dres && d_dsum && !in_place_ok(d_dres, ld_dres, 0, d_dsum, ld_dsum, 0)) ||
-            (d_dx && !in_place_ok(d_dx, ld_dx, 0, d_dy, ld_dy, 0)))
-            return PC_ERR_INVALID_ARG;
+        // in the place of an input's row, element by element, or in none
+        const struct { const void *p; size_t ld; int type; } rows_in[] = {
+            {d_dy, ld_dy, dtype}, {d_sum, ld_sum, sum_dtype}, {d_dsum, ld_dsum, sum_dtype}};
+        for (const auto &in : rows_in) {
+            if ((d_dres && !in_place_ok(d_dres, ld_dres, sum_dtype, in.p, in.ld, in.type)) ||
+                (d_dx && !in_place_ok(d_dx, ld_dx, dtype, in.p, in.ld, in.type)))
+                return PC_ERR_INVALID_ARG;
+            if (d_dweight && d_dweight == in.p) return PC_ERR_INVALID_ARG;
+        }
+        const void *others[] = {d_weight, d_rstd, stored_sum ? stored_sum->sym : nullptr,
+                                stored_sum ? stored_sum->scale : nullptr};
+        for (const void *in : others)
+            if (in && (d_dres == in || d_dx == in || d_dweight == in)) return PC_ERR_INVALID_ARG;
+        if (d_dweight && (d_dweight == d_dres || d_dweight == d_dx)) return PC_ERR_INVALID_ARG;
+        if (d_dres && d_dres == d_dx && (mask || sum_dtype != dtype || ld_dres != ld_dx)) return PC_ERR_INVALID_ARG;
     }
     if (!size_ok(rows, cols) || !size_ok(1, cols) ||
         (rows && (!span_ok(rows, ld_dy) || (d_sum && !span_ok(rows, ld_sum)) ||

@@ -225,7 +225,7 @@ hipError_t launch_rmsnorm_backward(const RmsNormGrad &c, hipStream_t stream) {
     a.ld_partial = partial_width(c.cols);
     a.cols = (uint32_t)c.cols;
     a.team = p.team;
-    p.columns_first = (c.d_x && c.d_x == c.dy) || (c.d_res && (c.d_res == c.sum || c.d_res == c.dy));
+    p.columns_first = (c.d_x && (c.d_x == c.sum || c.d_x == c.dy)) || (c.d_res && (c.d_res == c.sum || c.d_res == c.dy));
     a.per_col = (float)(1.0 / (double)c.cols);
     a.mask = mask_arg(c.mask);
     if (c.rows) {
