@@ -533,8 +533,10 @@ pc_status pc_dropout(const void *d_x, int dtype, size_t rows, size_t cols, size_
  *            from h in 64 bits, rounded once; what f32 cannot hold counts as infinite.
  *   d_y      NULL, or receives y rounded to y_dtype (from 32 bits, which have y
  *            to 3.1 2^-24 of it or 2^-126); where y_stored, the stored values in
- *            its place, as pc_q8_load gives them (needs d_sym).
+ *            its place, as pc_q8_load gives them (needs d_sym).  May be d_x or
+ *            d_res of its type (same ld).
  *   d_rstd   NULL, or receives rows f32.
+ * No output overlaps an input or another output but for what is said here.
  * Squares are summed in 64 bits.  A row that holds an infinity has rstd 0, one
  * that holds NaN has rstd NaN.  cols is below 2^31; cols == 0 writes nothing, rstd neither.
  */
@@ -606,7 +608,7 @@ pc_status pc_logprobs(const void *d_logits, int dtype, size_t rows, size_t vocab
  *   d_dlogp   rows x n_tokens f32 (NULL where n_tokens is 0).  Of a token
  *             equal to `padding` or outside the vocabulary it is not used.
  *   d_dentropy  NULL, or rows f32.
- *   d_dlogits rows x vocab of the logits' dtype; may be d_logits (same ld).
+ *   d_dlogits rows x vocab of the logits' dtype; may be d_logits (same ld), and overlaps no other input.
  * Rows whose given gradients are all 0 get zeros, whatever their logits; so do
  * rows that are -infinity throughout.
  */

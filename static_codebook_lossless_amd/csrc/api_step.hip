@@ -69,6 +69,15 @@ pc_status pc_rmsnorm_store(const void *d_x, int dtype, size_t rows, size_t cols,
     if (d_sum && (!in_place_ok(d_sum, ld_sum, sum_dtype, d_x, ldx, dtype) ||
                   !in_place_ok(d_sum, ld_sum, sum_dtype, d_res, ld_res, sum_dtype)))
         return PC_ERR_INVALID_ARG;
+    if (d_y && (!in_place_ok(d_y, ld_y, y_dtype, d_x, ldx, dtype) ||
+                !in_place_ok(d_y, ld_y, y_dtype, d_res, ld_res, sum_dtype) || d_y == d_sum))
+        return PC_ERR_INVALID_ARG;
+    const void *others[] = {d_x, d_res, d_weight, d_sum, d_y, d_counts};
+    for (const void *p : others)
+        if (p && (p == d_sym || p == d_scale || p == d_rstd)) return PC_ERR_INVALID_ARG;
+    if ((d_weight && (d_weight == d_sum || d_weight == d_y)) || (d_sym && (d_sym == d_scale || d_sym == (void *)d_rstd)) ||
+        (d_scale && d_scale == (void *)d_rstd))
+        return PC_ERR_INVALID_ARG;
     if (!size_ok(rows, cols) || !span_ok(rows, ldx) || (d_res && !span_ok(rows, ld_res)) ||
         (d_sum && !span_ok(rows, ld_sum)) || (d_y && !span_ok(rows, ld_y)))
         return PC_ERR_UNSUPPORTED;
@@ -241,6 +250,8 @@ pc_status pc_logprobs_backward(const void *d_logits, int dtype, size_t rows, siz
     if (!in_place_ok(d_logits, ld, 0, d_dlogits, ld_out, 0)) return PC_ERR_INVALID_ARG;
     if (!d_stats || !aligned(d_stats, 4) || !aligned(d_dlogp, 4) || !aligned(d_dentropy, 4)) return PC_ERR_INVALID_ARG;
     if (n_tokens && !d_dlogp) return PC_ERR_INVALID_ARG;
+    if (d_dlogits == d_stats || (n_tokens && (d_dlogits == d_tokens || d_dlogits == d_dlogp)) || d_dlogits == d_dentropy)
+        return PC_ERR_INVALID_ARG;
     if (n_tokens > kMaxPicked || !logits_size_ok(rows, vocab) || !span_ok(rows, ld) || !span_ok(rows, ld_out))
         return PC_ERR_UNSUPPORTED;
     pc::LogProbsGrad c = {};

@@ -45,3 +45,20 @@ def test_gradients_over_inputs(rows, cols, dtype, res):
                                      ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
         assert st == pc.PC_OK
         assert torch.equal(d_res, want.residual) and torch.equal(d_x, want.x) and torch.equal(dw, want.weight)
+
+
+@pytest.mark.parametrize("rows,cols", [(70, 264), (300, 96), (9, 8192), (3, 16390), (3, 40001)])
+@pytest.mark.parametrize("with_sum", [True, False])
+def test_y_over_inputs(rows, cols, with_sum):
+    lib = pc._lib.lib
+    rng = np.random.default_rng(82)
+    given = [activation(rng, rows, cols, "bf16") for _ in range(2)]
+    mask = pc.DropoutMask(0.3, 4)
+    want = pc.pc_rmsnorm_store(given[0], None, given[1], mask, y="plain")
+    for k in range(2):
+        x, res = (t.clone() for t in given)
+        y, total = (x, res)[k], torch.empty_like(x) if with_sum else None
+        st = lib.pc_rmsnorm_store(x.data_ptr(), pc.PC_BF16, rows, cols, cols, res.data_ptr(), pc.PC_BF16, cols, mask.arg,
+                                  None, 0, 1e-6, None if total is None else total.data_ptr(), cols, 0, None, None, None,
+                                  y.data_ptr(), pc.PC_BF16, cols, 0, None, torch.cuda.current_stream().cuda_stream)
+        assert st == pc.PC_OK and torch.equal(y, want.y) and (total is None or torch.equal(total, want.sum))

@@ -1,11 +1,11 @@
-"""Outputs of the norm's backward pass in an input's place: those that the header
+"""Outputs of the norm and of the logits' gradient in an input's place: those that the header
 allows are accepted, the others refused (on the CPU, by addresses that are never
 dereferenced)."""
 import itertools
 
 import pytest
 
-from test_step_args import A, BAD, BF16, F32, SMALL, back, mask, q8
+from test_step_args import A, BAD, BF16, BIG, F32, SMALL, back, logp_back, mask, norm, q8
 
 IN = {"dy": A, "total": 2 * A, "w": 3 * A, "rstd": 4 * A, "ds": 5 * A}
 ROWS = ("dy", "total", "ds")
@@ -59,3 +59,30 @@ def test_no_two_outputs_in_one_place():
 def test_both_in_place(a, b):
     assert back(dres=IN[a], dx=IN[b], **WIDE) == SMALL
     assert back(dres=IN[a], dx=IN[a], m=mask(), **WIDE) == BAD
+
+
+# the forward pass and the logits' gradient: accepted calls are recognised by an alignment that is refused later,
+# or by a row distance that is too large
+
+FAR = dict(rows=1 << 20, ld=1 << 45)
+
+
+def test_y_in_place():
+    far = dict(rows=1 << 20, ld=1 << 45, ldr=1 << 45, ldy=1 << 45, lds=64)
+    assert norm(**far) == BIG and norm(y=A, **far) == BIG and norm(y=2 * A, **far) == BIG
+    assert norm(y=A, **{**far, "ldy": 64}) == BAD and norm(y=2 * A, **{**far, "ldy": 64}) == BAD
+    assert norm(y=A, yd=F32, **far) == BAD and norm(y=2 * A, sum_dtype=F32, **far) == BAD
+    assert norm(y=4 * A, **{**far, "ldy": 64}) == BAD  # the sum's place
+
+
+@pytest.mark.parametrize("kw", [dict(sym=A), dict(scale=2 * A), dict(rstd=A), dict(sym=3 * A), dict(rstd=4 * A), dict(rstd=7 * A),
+                                dict(scale=5 * A), dict(rstd=5 * A), dict(rstd=6 * A), dict(counts=5 * A), dict(total=3 * A),
+                                dict(y=3 * A)])
+def test_norm_outputs_of_their_own(kw):
+    assert norm(**FAR) == BIG and norm(**kw, **FAR) == BAD
+
+
+@pytest.mark.parametrize("out", [2, 3, 4, 5])
+def test_no_logits_gradient_over_its_other_inputs(out):
+    assert logp_back(out=A, ldo=1 << 45, **FAR) == BIG and logp_back(out=6 * A, **FAR) == BIG
+    assert logp_back(out=out * A, **FAR) == BAD
