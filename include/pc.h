@@ -504,7 +504,8 @@ pc_status pc_embed_backward(const void *d_dy, int dy_dtype, size_t ld_dy, const 
  *   p         0 (nothing is dropped) to 1 (everything is).
  *   d_random  NULL, or two u64 in device memory (8-byte aligned): the seed, in
  *             place of `seed`, and a number added to `offset` modulo 2^64.  A
- *             captured graph reads them anew at each replay.
+ *             captured graph reads them anew at each replay; they stay as they
+ *             are until the backward pass that takes the mask again has run.
  * Calls that shall not share a mask differ in seed or offset.  The struct is host memory, read during the call.
  */
 typedef struct pc_mask {

@@ -27,8 +27,11 @@ class DropoutMask:
     or offset differs: a layer's number and a step's make a good offset.
 
     ``seed`` may be an int64 device tensor of two numbers, the seed and one
-    that is added to ``offset`` (both modulo 2**64): kernels read it, so a
-    captured graph draws new masks when it changes.  ``p`` is taken to the
+    that is added to ``offset`` (both modulo 2**64): kernels read it where it
+    is at the call, so a captured graph draws new masks when it changes.  The
+    backward pass reads it too: its numbers have to stay until that has run
+    (with several steps in flight, each takes a tensor of its own, or an
+    ``offset``).  ``p`` is taken to the
     nearest multiple of 2**-16; what is not dropped is divided by the share
     that stays."""
 
@@ -43,9 +46,7 @@ class DropoutMask:
             raise ValueError("offset must have 64 bits")
         where = None
         if isinstance(seed, torch.Tensor):
-            if not seed.is_cuda or seed.dtype != torch.int64 or seed.shape != (2,) or not seed.is_contiguous():
-                raise TypeError("a seed on the device must be two contiguous int64")
-            value, where = 0, seed.data_ptr()
+            value, where = 0, _seed_address(seed)
         else:
             value = operator.index(seed)
             if not 0 <= value < 1 << 64:
@@ -54,15 +55,25 @@ class DropoutMask:
         self.arg = MaskArg(p, value, offset, where)
 
 
+def _seed_address(seed):
+    if not seed.is_cuda or seed.dtype != torch.int64 or seed.shape != (2,) or not seed.is_contiguous():
+        raise TypeError("a seed on the device must be two contiguous int64")
+    return seed.data_ptr()
+
+
 def _mask(mask, device):
     """The mask's argument (None without one)."""
     if mask is None:
         return None
     if not isinstance(mask, DropoutMask):
         raise TypeError("mask must be a DropoutMask, not %s" % type(mask).__name__)
-    if mask.arg.d_random and mask.seed.device != device:
+    if not mask.arg.d_random:
+        return mask.arg
+    # where the tensor is now: its memory may have been replaced since (``set_``, ``.data``)
+    where = _seed_address(mask.seed)
+    if mask.seed.device != device:
         raise ValueError("the mask's seed is on %s, not on %s" % (mask.seed.device, device))
-    return mask.arg
+    return mask.arg if mask.arg.d_random == where else MaskArg(mask.p, 0, mask.offset, where)
 
 
 def pc_dropout(x, mask: DropoutMask, out=None) -> torch.Tensor:
