@@ -100,7 +100,8 @@ class LogProbs(torch.autograd.Function):
     @staticmethod
     def backward(ctx, d_logp, d_entropy):
         logits, tokens, stats = ctx.saved_tensors
-        # nothing reads the logits any more: their gradient takes their place
+        # nothing here reads the logits any more, so their gradient takes their place; a second backward
+        # pass, or another loss that has saved them, gets autograd's error of a tensor modified in place
         return pc.pc_logprobs_backward(logits, stats, tokens, d_logp.contiguous(), d_entropy.contiguous(),
                                        out=logits.detach()), None
 

@@ -5,6 +5,10 @@ float32, float16 or bfloat16 rows of unit stride, wrong types, sizes, strides
 or devices raise ``TypeError`` or ``ValueError``, and what the library itself
 refuses raises ``PcError``.  Tensors of more than two dimensions count as rows
 of their last one, and what is returned has their shape.
+
+Tensors that a caller gives to be written (``out``, ``sum_out``,
+``weight_out``) count as changed in place: where an autograd graph has saved
+one, its backward pass raises torch's error instead of using what was written.
 """
 from __future__ import annotations
 
@@ -86,8 +90,11 @@ def pc_dropout(x, mask: DropoutMask, out=None) -> torch.Tensor:
         raise TypeError("mask must be a DropoutMask")
     device = x.device
     arg = _mask(mask, device)
+    given = out is not None
     out, to, ld_out = _like(out, x, x.dtype, cols, "out")
     _launch("pc_dropout", device, lib.pc_dropout, where, kind, n, cols, ld, arg, to, ld_out)
+    if given:
+        _written(out)
     return out
 
 
@@ -114,6 +121,10 @@ def _like(out, x, dtype, cols, what):
         return out, out.data_ptr(), cols
     where, ld = _same_rows(out, x, dtype, what)
     return out, where, ld
+
+
+# kernels write by address: what torch's own in-place operations do to a tensor's version
+_written = torch.autograd.graph.increment_version
 
 
 def _same_rows(t, x, dtype, what):
@@ -214,6 +225,8 @@ def pc_rmsnorm_store(x, weight=None, residual=None, mask=None, eps=1e-6, format=
     _launch("pc_rmsnorm_store", device, lib.pc_rmsnorm_store, at, kind, n, cols, ldx, res,
             _DTYPES[sum_dtype], ld_res, arg, w, w_kind, eps, where, ld_sum, code, sym, scale,
             None if counts is None else counts.data_ptr(), to, to_kind, cols, int(y == "stored"), rstd.data_ptr())
+    if sum_out is not None:
+        _written(sum_out)
     return RmsNorm(q, out, total, rstd)
 
 
@@ -287,6 +300,8 @@ def pc_rmsnorm_backward(dy, sum, weight, rstd, d_sum=None, mask=None, dtype=None
             _DTYPES[dtype], kept_ld, stored, w, w_kind, rstd.data_ptr(), ds, ld_ds, arg, residual.data_ptr(), cols,
             d_x, cols, None if d_weight is None else d_weight.data_ptr(), out_kind, int(accumulate),
             None if ws is None else ws.data_ptr(), need)
+    if weight_out is not None:
+        _written(weight_out)
     return RmsNormGrads(residual, x, d_weight)
 
 
@@ -373,7 +388,8 @@ def pc_logprobs_backward(logits, stats, tokens=None, d_logp=None, d_entropy=None
     (``d_logp``, of the tokens' shape) and entropy (``d_entropy``), both
     float32.  ``stats``, ``tokens``, ``scale`` and ``padding`` are the forward
     pass's.  ``out`` (of the logits' shape and dtype) receives it and may be
-    ``logits``."""
+    ``logits``, where nothing reads these any more: no second backward pass, no
+    other loss that has saved them."""
     kind, scale, padding = _dtype(logits.dtype, "logits"), float(scale), operator.index(padding)
     at, n, vocab, ld = _flat(logits, "logits")
     device, lead = logits.device, logits.shape[:-1]
@@ -390,10 +406,13 @@ def pc_logprobs_backward(logits, stats, tokens=None, d_logp=None, d_entropy=None
         d_logp = _gradient(d_logp, tokens.shape, logits, "d_logp")
     if d_entropy is not None:
         d_entropy = _gradient(d_entropy, lead, logits, "d_entropy")
+    given = out is not None
     out, to, ld_out = _like(out, logits, logits.dtype, vocab, "out")
     _launch("pc_logprobs_backward", device, lib.pc_logprobs_backward, at, kind, n, vocab, ld, scale,
             stats.data_ptr(), where, width, m, padding, None if d_logp is None else d_logp.data_ptr(),
             None if d_entropy is None else d_entropy.data_ptr(), to, ld_out)
+    if given:
+        _written(out)
     return out
 
 

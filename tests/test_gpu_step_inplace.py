@@ -1,8 +1,13 @@
-"""Tensors whose memory changes between calls."""
+"""Tensors whose memory or contents change between calls, and who hears of it."""
+import importlib.util
+import os
+
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_step import DEV
+from conftest import ROOT
+from test_gpu_step import DEV, activation
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +44,46 @@ def test_mask_refuses_a_seed_that_no_longer_fits():
         seed.set_(other)
         with pytest.raises(TypeError):
             pc.pc_dropout(x, mask)
+
+
+def writes():
+    """(what is written, a call that writes it) for every output that a caller gives."""
+    rng = np.random.default_rng(71)
+    x = activation(rng, 6, 64, "f32")
+    w, rstd, mask = torch.rand(64, device=DEV), torch.rand(6, device=DEV), pc.DropoutMask(0.5, 1)
+    tokens = torch.arange(6, device=DEV)
+    stats = pc.pc_logprobs(x, tokens).stats
+    d = torch.ones(6, device=DEV)
+    return [
+        (x, lambda out: pc.pc_dropout(x, mask, out=out)),
+        (x, lambda out: pc.pc_rmsnorm_store(x, w, residual=x, sum_out=out)),
+        (x, lambda out: pc.pc_logprobs_backward(x, stats, tokens, d, out=out)),
+        (torch.zeros(64, device=DEV), lambda out: pc.pc_rmsnorm_backward(x, x, w, rstd, weight_out=out)),
+        (torch.zeros(64, device=DEV), lambda out: pc.pc_rmsnorm_backward(x, x, w, rstd, weight_out=out, accumulate=True)),
+    ]
+
+
+@pytest.mark.parametrize("k", range(5))
+def test_writes_are_seen_by_autograd(k):
+    """A tensor that a graph has saved and a call has written since is reported, not used."""
+    like, call = writes()[k]
+    out = (like.clone().requires_grad_() * 1.0)
+    loss = out.square().sum()  # saves out
+    call(out.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    # in inference mode nothing is counted, and the calls work
+    with torch.inference_mode():
+        call(like.clone())
+
+
+def test_example_reports_a_second_backward_pass():
+    spec = importlib.util.spec_from_file_location("residual_step", os.path.join(ROOT, "examples", "residual_step.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    model = example.Model(vocab=64, dim=32, hidden=32)
+    tokens = torch.arange(64, device=DEV)
+    loss = model.loss(tokens, tokens, torch.ones(64, device=DEV))
+    loss.backward(retain_graph=True)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
