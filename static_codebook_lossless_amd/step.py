@@ -336,6 +336,13 @@ def pc_logprobs_workspace_bytes(rows, vocab, top=0, dtype=PC_BF16):
     return int(lib.pc_logprobs_workspace_bytes(rows, vocab, top, dtype))
 
 
+def _padding(padding):
+    padding = operator.index(padding)
+    if not -1 << 63 <= padding < 1 << 63:
+        raise ValueError("padding must have 64 bits, with its sign")
+    return padding
+
+
 def _picked(tokens, lead, device):
     """(tokens, how many each row has) for rows of the shape ``lead``."""
     tokens = _tokens(tokens, device)
@@ -355,7 +362,7 @@ def pc_logprobs(logits, tokens=None, top=0, scale=1.0, padding=-1, status=None) 
     vocabulary gets 0 and, unless it is the padding, sets ``status`` (int32 [1]
     on the device, zeroed by the caller) to ``PC_ERR_INVALID_ARG``.  Equal
     logits are ordered by their index."""
-    kind, scale, padding, top = _dtype(logits.dtype, "logits"), float(scale), operator.index(padding), operator.index(top)
+    kind, scale, padding, top = _dtype(logits.dtype, "logits"), float(scale), _padding(padding), operator.index(top)
     at, n, vocab, ld = _flat(logits, "logits")
     device, lead = logits.device, logits.shape[:-1]
     logp, where, m, width = None, None, 0, 8
@@ -390,7 +397,7 @@ def pc_logprobs_backward(logits, stats, tokens=None, d_logp=None, d_entropy=None
     pass's.  ``out`` (of the logits' shape and dtype) receives it and may be
     ``logits``, where nothing reads these any more: no second backward pass, no
     other loss that has saved them."""
-    kind, scale, padding = _dtype(logits.dtype, "logits"), float(scale), operator.index(padding)
+    kind, scale, padding = _dtype(logits.dtype, "logits"), float(scale), _padding(padding)
     at, n, vocab, ld = _flat(logits, "logits")
     device, lead = logits.device, logits.shape[:-1]
     if stats.dtype != torch.float32 or stats.shape != (n, 4) or not stats.is_contiguous():
