@@ -37,9 +37,10 @@ class DropoutMask:
     (with several steps in flight, each takes a tensor of its own, or an
     ``offset``).  ``p`` is taken to the
     nearest multiple of 2**-16; what is not dropped is divided by the share
-    that stays."""
+    that stays.  A mask is what it was made of: another ``p``, ``seed`` or
+    ``offset`` is another object."""
 
-    __slots__ = ("p", "seed", "offset", "arg")
+    __slots__ = ("_p", "_seed", "_offset", "arg")
 
     def __init__(self, p, seed=0, offset=0):
         p = float(p)
@@ -55,8 +56,12 @@ class DropoutMask:
             value = operator.index(seed)
             if not 0 <= value < 1 << 64:
                 raise ValueError("seed must have 64 bits")
-        self.p, self.seed, self.offset = p, seed, offset
+        self._p, self._seed, self._offset = p, seed, offset
         self.arg = MaskArg(p, value, offset, where)
+
+    p = property(lambda self: self._p)
+    seed = property(lambda self: self._seed)
+    offset = property(lambda self: self._offset)
 
 
 def _seed_address(seed):
@@ -74,10 +79,11 @@ def _mask(mask, device):
     if not mask.arg.d_random:
         return mask.arg
     # where the tensor is now: its memory may have been replaced since (``set_``, ``.data``)
-    where = _seed_address(mask.seed)
-    if mask.seed.device != device:
-        raise ValueError("the mask's seed is on %s, not on %s" % (mask.seed.device, device))
-    return mask.arg if mask.arg.d_random == where else MaskArg(mask.p, 0, mask.offset, where)
+    seed = mask._seed
+    where = _seed_address(seed)
+    if seed.device != device:
+        raise ValueError("the mask's seed is on %s, not on %s" % (seed.device, device))
+    return mask.arg if mask.arg.d_random == where else MaskArg(mask._p, 0, mask._offset, where)
 
 
 def pc_dropout(x, mask: DropoutMask, out=None) -> torch.Tensor:
