@@ -243,45 +243,52 @@ __device__ __forceinline__ void norm_unit(const NormArgs &a, uint64_t row, uint3
         heavy = fmaxf(heavy, fabsf(w[i]));
     }
     const bool faint = FAINT && (heavy > kFaintWeight || r < kNormal), above_1 = FAINT && heavy > 1.0f;
-    auto precise = [&](auto round) {
+    const bool plain = a.y && !a.y_stored && n, e4m3 = a.format == PC_Q8_E4M3;
+    if (plain) store_any(a.y_kind, a.y, row * a.ld_y + col, n, y);
+    // y is off by 3.1 2^-24 at most; where that could change what is stored (one unit of
+    // a wave in 150 or so), the wave forms it again in 64 bits, so that nothing but
+    // the rounding to 8 bits shows
+    bool unsure = faint;
+    uint32_t code = 0;
+    u32x2 s = {0, 0};
+    if (a.sym) {
+        bool may;
+        s = e4m3 ? to_stored<PC_Q8_E4M3, true>(y, code, &may) : to_stored<PC_Q8_INT8, true>(y, code, &may);
+        unsure |= may || (above_1 && code <= kFaintCode);
+    }
+    if (__ballot(unsure)) {
         float h2[8], w2[8];
         again(h2, w2);
+        double v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = round((double)h2[i] * rstd * (double)w2[i]);
-    };
-    if (faint && a.y && !a.y_stored) precise([](double v) { return (float)v; });
-    if (a.y && !a.y_stored && n) store_any(a.y_kind, a.y, row * a.ld_y + col, n, y);
+        for (int i = 0; i < 8; ++i) v[i] = (double)h2[i] * rstd * (double)w2[i];
+        if (faint && plain) {  // once more, over the first
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = (float)v[i];
+            store_any(a.y_kind, a.y, row * a.ld_y + col, n, y);
+        }
+        if (a.sym) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = rounded_to_odd(v[i]);
+            s = e4m3 ? to_stored<PC_Q8_E4M3>(y, code) : to_stored<PC_Q8_INT8>(y, code);
+        }
+    }
     if (!a.sym) return;
-    auto store = [&](auto f) {
-        constexpr int FMT = decltype(f)::value;
-        // y is off by 3.1 2^-24 at most; where that could change what is stored (one unit of
-        // a wave in 150 or so), the wave forms it again in 64 bits, so that nothing but
-        // the rounding to 8 bits shows
-        uint32_t code;
-        bool unsure;
-        u32x2 s = to_stored<FMT, true>(y, code, &unsure);
-        unsure |= faint || (above_1 && code <= kFaintCode);
-        if (__ballot(unsure)) {
-            precise(rounded_to_odd);
-            s = to_stored<FMT>(y, code);
+    if (n) {
+        store_symbols(a.sym + row * a.cols + col, n, s);
+        if (col % kGroup == 0) a.scale[row * a.groups + col / kGroup] = (uint8_t)code;
+        if (a.y && a.y_stored) {
+            float v[8];
+            if (e4m3) unit_values<PC_Q8_E4M3>(s, scale_of(code), v);
+            else unit_values<PC_Q8_INT8>(s, scale_of(code), v);
+            store_any(a.y_kind, a.y, row * a.ld_y + col, n, v);
         }
-        if (n) {
-            store_symbols(a.sym + row * a.cols + col, n, s);
-            if (col % kGroup == 0) a.scale[row * a.groups + col / kGroup] = (uint8_t)code;
-            if (a.y && a.y_stored) {
-                float v[8];
-                unit_values<FMT>(s, scale_of(code), v);
-                store_any(a.y_kind, a.y, row * a.ld_y + col, n, v);
-            }
-        }
-        if constexpr (COUNT) {
+    }
+    if constexpr (COUNT) {
 #pragma unroll
-            for (uint32_t i = 0; i < kUnit; ++i)
-                if (i < n) atomicAdd(&bins[(s[i / 4] >> (8 * (i % 4))) & 0xFF], 1u);
-        }
-    };
-    if (a.format == PC_Q8_E4M3) store(std::integral_constant<int, PC_Q8_E4M3>());
-    else store(std::integral_constant<int, PC_Q8_INT8>());
+        for (uint32_t i = 0; i < kUnit; ++i)
+            if (i < n) atomicAdd(&bins[(s[i / 4] >> (8 * (i % 4))) & 0xFF], 1u);
+    }
 }
 
 // A team takes a row into its registers, so that x, the residual and the mask's
