@@ -564,6 +564,7 @@ pc_status pc_rmsnorm_store(const void *d_x, int dtype, size_t rows, size_t cols,
  *            is summed in 32 bits in an order that depends on the sizes alone.
  *   d_ws, ws_bytes  scratch of pc_rmsnorm_backward_workspace_bytes (0 for few
  *            rows, then d_ws may be NULL), 16-byte aligned; not needed without d_dweight.
+ * Computed in 32 bits: an n below 2^-126 (a small h in a row of large ones) is off by 2^-150.
  * rows == 0: d_weight = 0, or stays where accumulate.
  */
 size_t pc_rmsnorm_backward_workspace_bytes(size_t rows, size_t cols);

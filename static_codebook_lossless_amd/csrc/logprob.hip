@@ -520,7 +520,8 @@ __device__ __forceinline__ uint64_t largest_elements(const Args &a, const typena
 // A workgroup takes a row, or one of `splits` stretches of it: a batch of
 // elements gives a maximum first, for which the sums so far are moved if it is
 // a new one, then an exponential and two sums an element.  4096 x 128000 bf16:
-// 170 us, 6.2 TB/s, with vector work in all of the cycles; 511 x 32001 f32 with 4
+// 170-172 us a pass of many, 6.1 TB/s (176-191 alone in a trace), with vector work
+// in all of the cycles; 511 x 32001 f32 with 4
 // tokens and 5 alternatives: 18 us, two workgroups to a CU, 13 without the
 // alternatives; 1 x 128000 with 20: 9.4 us in 31 stretches, and 4.8 for the join.
 template <int DT, bool TOP, bool STREAM, uint32_t THREADS>

@@ -22,7 +22,7 @@ struct NormArgs {
     float *rstd;
     uint64_t rows, ldx, ld_res, ld_sum, ld_y;
     uint32_t cols, groups;
-    uint32_t team;  // lanes to a row: whole waves
+    uint32_t team;  // lanes to a row: whole waves, or 16 or 32 of one
     int weight_kind, y_kind, format, y_stored;
     double eps, per_col;  // per_col: 1 / cols
     MaskArg mask;
@@ -33,7 +33,7 @@ struct GradArgs {
     const uint8_t *sym, *scale;  // the sum in its stored form, in place of `sum`
     const float *rstd;
     void *d_res, *d_x;
-    float *partial;  // [teams of all workgroups][ld_partial], or nullptr
+    float *partial;  // partial sums, [GradPlan::parts][ld_partial] (a row for each workgroup, or for each wave where rows are long), or nullptr
     uint64_t rows, ld_dy, ld_sum, ld_sym, ld_scale, ld_d_sum, ld_d_res, ld_d_x, ld_partial;
     uint32_t cols, team;
     int weight_kind, format;

@@ -121,9 +121,12 @@ GradPlan plan_grad(uint64_t rows, uint64_t cols, bool f32, uint64_t bytes) {
     return p;
 }
 
-// Rows and columns in one launch, by sizes alone.  With the host's share, in one
-// launch and in two: 512 x 8192 12.4 and 17.1 us, 512 x 1024 11.7 and 15.8, 1024 x
-// 1024 14.8 and 15.8 but 15.1 and 8.6 on the device, 2048 x 2048 39 and 17.
+// Rows and columns in one launch, by sizes alone.  bf16, in one launch and in two,
+// on the device with inputs from HBM (as a captured step has it) and with the host's
+// share of an eager pass: 128 x 2048 5.0 and 7.2, 10.6 and 14.9 us; 512 x 8192 15.5 and
+// 17.2, 15.1 and 16.9; 512 x 4096 10.2 and 16.6, 10.8 and 16.3; 512 x 1024 11.6 and 7.4,
+// 11.3 and 14.8: narrow rows gain with the host's share alone.  Beyond the rule one launch
+// is the slower one: 1024 x 1024 on the device 15.1 and 8.6, 2048 x 2048 39 and 17.
 constexpr uint64_t kOnceRows = 512, kOnceElements = 1ull << 22;
 
 bool once_fits(uint64_t rows, uint64_t cols) {

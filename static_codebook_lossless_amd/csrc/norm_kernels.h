@@ -294,8 +294,8 @@ __device__ __forceinline__ void norm_unit(const NormArgs &a, uint64_t row, uint3
 // A team takes a row into its registers, so that x, the residual and the mask's
 // numbers are read and formed once.  U units a lane; LONG: rows of more than
 // team * U units, read in turns.  8192 x 8192 bf16 with a residual and a mask,
-// to e4m3 and the stored y: 102 us, 6.0 TB/s beside vector work in 84% of the
-// cycles; 8192 x 4096 without the mask, to e4m3 and y: 54 us, 5.6 TB/s.  Bounds
+// to e4m3 and the stored y: 102-103 us, 5.9 TB/s beside vector work in 84% of the
+// cycles; 8192 x 4096 without the mask, to e4m3 and y: 57 us, 5.3 TB/s.  Bounds
 // on waves for the registers are not asked for: the compiler then spills (150 us).
 template <int DT, int RT, int U, uint32_t SUB, bool COUNT, bool LONG, bool STREAM, bool WHOLE>
 __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs a) {
@@ -491,8 +491,8 @@ __device__ __forceinline__ void forget_kept(KeptUnit<RT, STORED> &k) {
 // A team takes every (grid * teams)th row and sums the weight's gradient over
 // them in its registers; the next row's tensors are on their way while a row
 // is worked on.  A workgroup's teams join their sums in LDS, in order.  8192 x
-// 8192 bf16, the sum in e4m3, with a mask: 102-105 us, 5.4 TB/s with the partial
-// sums' 16 MiB, vector work in 61% of the cycles.
+// 8192 bf16, the sum in e4m3, with a mask: 102-109 us, 5.7-6.1 TB/s with the partial
+// sums' 16 MiB, vector work in 59% of the cycles.
 template <int DT, int RT, int U, uint32_t SUB, bool STORED, bool STREAM, bool WHOLE>
 __device__ __forceinline__ void grad_rows(const GradArgs &a, uint32_t blocks) {
     typedef typename Plain<DT>::type TX;
@@ -647,7 +647,8 @@ __device__ __forceinline__ void grad_columns(const GradArgs &a, uint32_t block) 
 // Few rows in one launch: some workgroups take rows, the others columns, which
 // need nothing of each other: the weight's gradient reads dy and the sum again,
 // but has no partial sums, and the call no second launch and no workspace (128
-// x 2048 f16 with the host's share: 15.7 us, in one launch 11).
+// x 2048 bf16 with the host's share: 14.9 us, in one launch 10.6; on the device 7.2
+// and 5.0).
 template <int DT, int RT, bool STORED>
 __global__ __launch_bounds__(kMaxThreads) void norm_grad_once_kernel(GradArgs a) {
     if (blockIdx.x < a.row_blocks) grad_rows<DT, RT, 1, kWave, STORED, false, false>(a, a.row_blocks);
@@ -655,7 +656,8 @@ __global__ __launch_bounds__(kMaxThreads) void norm_grad_once_kernel(GradArgs a)
 }
 
 // Rows of more units than a workgroup's registers hold, read twice (2048 x 40000
-// bf16 with the weight's gradient: 227 us, at one reading's bytes 2.9 TB/s).
+// bf16 with the weight's gradient: 233 us, at one reading's bytes 2.8 TB/s; 4096 x
+// 16384 with an f32 sum: 305 us, 3.5 TB/s).
 template <int DT, int RT, bool STORED>
 __global__ __launch_bounds__(kMaxThreads) void norm_grad_long_kernel(GradArgs a) {
     typedef typename Plain<DT>::type TX;
