@@ -611,8 +611,8 @@ pc_status pc_logprobs(const void *d_logits, int dtype, size_t rows, size_t vocab
  *             equal to `padding` or outside the vocabulary it is not used.
  *   d_dentropy  NULL, or rows f32.
  *   d_dlogits rows x vocab of the logits' dtype; may be d_logits (same ld), and overlaps no other input.
- * Rows whose given gradients are all 0 get zeros, whatever their logits; so do
- * rows that are -infinity throughout.
+ * Probabilities below 2^-126 count as 0.  Rows whose given gradients are all 0
+ * get zeros, whatever their logits; so do rows that are -infinity throughout.
  */
 pc_status pc_logprobs_backward(const void *d_logits, int dtype, size_t rows, size_t vocab, size_t ld, float scale,
                                const float *d_stats, const void *d_tokens, int token_bytes, size_t n_tokens,
